@@ -48,7 +48,8 @@ typedef enum {
                               was coded with (hash mismatch), or shape mismatch  */
     SKV_ERR_DEVICE = -6,   /* a HIP runtime call failed                           */
     SKV_ERR_NOMEM = -7,    /* host or device allocation failed                   */
-    SKV_ERR_BUSY = -8      /* a store entry is pinned (in use)                   */
+    SKV_ERR_BUSY = -8,     /* a store entry is pinned (in use)                   */
+    SKV_ERR_PAGES = -9     /* a length, start, page or slot was out of range     */
 } skv_status;
 
 typedef enum { SKV_BF16 = 1, SKV_E4M3 = 2, SKV_INT16 = 3 } skv_dtype;
@@ -396,6 +397,160 @@ int skv_store_decode(skv_store* store, const void* tables_blob, uint64_t entry, 
                      size_t* work_bytes, hipStream_t stream);
 int skv_store_erase(skv_store* store, uint64_t entry);
 int skv_store_stats(skv_store* store, skv_store_info* stats);
+
+/* Paged caches (device).  Where a restored or growing cache is used: the
+ * tokens of every request in pages of page_tokens tokens taken from one pool,
+ * found through a block table, so that requests grow without moving and share
+ * the pages of a common prefix ("Speculative KV coding" page, section "Where
+ * it can be used": prefix caching; a restored cache is used as the original,
+ * DCKV page, "How it works").  skv_page_plan builds a step's block tables and
+ * slot maps, skv_page_write puts rows (new tokens, or a decoded prefix) into
+ * pages, skv_page_read takes them out again in the layout that skv_encode
+ * codes, and skv_page_attention lets new tokens attend to what the pages hold.
+ *
+ * K and V of one layer are two arrays of the same strides,
+ *   [pages][page_tokens][heads][head_dim], head_dim contiguous,
+ * any of the other strides (in elements; each a multiple of 16 bytes, the
+ * base 16-byte aligned, else SKV_ERR_ARG), so head-major pools, slices of a
+ * whole-cache array [layers][K|V][...] and the codec's own contiguous arrays
+ * (pages of 128 consecutive tokens) all qualify.  dtype: SKV_BF16, or
+ * SKV_E4M3 with a scale per head, value = code * scale[head] (NULL: 1).
+ * page_tokens: a power of two, 8..1024.  heads * head_dim at most 65536,
+ * head_dim a multiple of 16 (attention: 64, 128 or 256); pages * page_tokens
+ * at most 2^31 - 1.  The layer stride counts for skv_page_write and
+ * skv_page_read, which take `layers` layers in one call.
+ *
+ * Every call only queues kernels on the stream: it allocates nothing, never
+ * waits, keeps no state between calls, and can be captured into a graph.
+ * Lengths, tables and slots are device data that the host never sees, so the
+ * kernels check them: what is out of range is never followed; the request,
+ * page or row concerned counts as empty, absent or skipped, as each call
+ * says, and a flag is OR-ed into *d_status (NULL: not recorded), which the
+ * caller clears.  skv_page_check waits for the stream and turns a non-zero
+ * status word into SKV_ERR_PAGES. */
+#define SKV_PAGES_LENGTH 1u   /* a length or start out of range                */
+#define SKV_PAGES_PAGE 2u     /* a block table names no page of the pool       */
+#define SKV_PAGES_SLOT 4u     /* a slot outside the pool                       */
+#define SKV_PAGES_FREE 8u     /* the free list ended before the requests did   */
+#define SKV_PAGES_ROWS 16u    /* more new tokens than the call has rows for    */
+typedef struct {
+    uint32_t abi_version;
+    uint32_t dtype;        /* of the pages: SKV_BF16 or SKV_E4M3 */
+    uint32_t layers;
+    uint32_t pages, page_tokens, heads, head_dim;
+    uint32_t zero;
+    int64_t layer_stride, page_stride, token_stride, head_stride;
+} skv_pages;
+typedef struct {           /* [layers][tokens][heads][head_dim] rows, K and V of the same strides */
+    uint32_t dtype;
+    uint32_t tokens;
+    int64_t layer_stride, token_stride, head_stride;
+} skv_rows;
+
+/* Block tables and slot maps of one step.  Request b has d_lens[b] tokens
+ * once the step is done, the last d_new[b] of them new.  With P =
+ * page_tokens, old = lens - new, have = ceil(old / P), want = ceil(lens / P):
+ *   taken[b]  = sum over earlier requests of want - have   (taken[requests] = all)
+ *   starts[b] = sum over earlier requests of new           (starts[requests] = all)
+ *   table[b][have + j] = free[taken[b] + j]                 (j < want - have)
+ *   positions[starts[b] + i] = old + i                      (i < new)
+ *   slots[starts[b] + i] = table[b][pos / P] * P + pos % P
+ * so packed row starts[b] + i is new token i of request b.  The first have
+ * entries of a table row are read, entries from want on are left alone.
+ * `tokens` rows of slots and positions are written; those from
+ * starts[requests] on receive -1, a slot that the other calls skip, so a
+ * step padded to a fixed row count can be captured once and replayed.  The
+ * caller takes taken[requests] pages off its list afterwards.  With d_free ==
+ * NULL nothing is taken (taken is all zero) and the table is only read: the
+ * slots of tokens that already have pages (lens = new: a request's whole
+ * cache).  requests 1..4096, width 1.. and width * page_tokens at most 2^31 -
+ * 1, tokens at most 2^31 - 1.
+ * A request with new < 0, lens < new or lens > width * P counts as new = 0
+ * with no pages (SKV_PAGES_LENGTH); blocks past the list's end get -1 in the
+ * table and their tokens slot -1 (SKV_PAGES_FREE), as do tokens whose table
+ * entry is negative or whose slot would pass 2^31 - 1 (SKV_PAGES_PAGE); new
+ * tokens past `tokens` get no row (SKV_PAGES_ROWS), and starts is cut at
+ * `tokens`. */
+int skv_page_plan(const int32_t* d_lens, const int32_t* d_new, uint32_t requests, int32_t* d_table, uint32_t width,
+                  int64_t table_stride, const int32_t* d_free, uint32_t free_pages, uint32_t page_tokens,
+                  uint32_t tokens, int32_t* d_slots, int32_t* d_positions, int32_t* d_starts, int32_t* d_taken,
+                  uint32_t* d_status, hipStream_t stream);
+
+/* Rows into pages: row t of every layer goes to slot d_slots[t] (page slot /
+ * P, token slot % P).  A negative slot skips its row; one past the pool skips
+ * it too (SKV_PAGES_SLOT).  A slot named by two rows receives, 16 bytes at a
+ * time, one of them.  bf16 rows into bf16 pages and e4m3 rows into e4m3 pages
+ * are copied (scales must be NULL: else SKV_ERR_ARG); bf16 rows into e4m3
+ * pages are divided by the head's scale in 32 bits and rounded to nearest,
+ * ties to even, values past +-448 to +-448, NaN to NaN (one rounding to 4
+ * significant bits: the cache's own type).  Other pairs: SKV_ERR_SHAPE.
+ * Rows and pages must not overlap. */
+int skv_page_write(const skv_pages* pages, void* d_k_pages, void* d_v_pages, const skv_rows* rows, const void* d_k,
+                   const void* d_v, const int32_t* d_slots, const float* d_k_scale, const float* d_v_scale,
+                   uint32_t* d_status, hipStream_t stream);
+
+/* Rows out of pages, the reverse: row t of every layer is slot d_slots[t]; a
+ * negative or (SKV_PAGES_SLOT) outlying slot gives a row of zeros.  bf16 to
+ * bf16 and e4m3 to e4m3 are copies (scales must be NULL), e4m3 pages to bf16
+ * rows are code * scale[head] in 32 bits rounded once to bf16. */
+int skv_page_read(const skv_pages* pages, const void* d_k_pages, const void* d_v_pages, const skv_rows* rows,
+                  void* d_k, void* d_v, const int32_t* d_slots, const float* d_k_scale, const float* d_v_scale,
+                  uint32_t* d_status, hipStream_t stream);
+
+/* Attention of new tokens over a paged cache.  Request b holds d_lens[b]
+ * tokens in the pages that d_table[b] names; its n = starts[b + 1] -
+ * starts[b] last ones are the queries, packed rows starts[b].. of d_q
+ * (d_starts NULL: one row per request, row b).  Query i of a request has
+ * position lens - n + i; query head h reads KV head h / (q_heads / heads):
+ *   s_j   = scale * q . (k_scale[head] * k_j)     j <= position (causal) or j < lens
+ *   out   = sum_j exp(s_j - lse) v_scale[head] v_j
+ *   lse   = log sum_j exp s_j                       (natural log; optional)
+ * from one new token per request to whole prompts (n = lens), any mix in one
+ * call.  A query that sees no key (position < 0, or lens = 0) gets zeros and
+ * lse = -infinity.  What a query does not see never reaches it, infinities and
+ * NaN included; what it sees propagates as the formula says.  Sums, maxima and
+ * products are held in 32 bits; the probabilities are rounded to bf16 for
+ * their product with V and the result once to bf16.  The same call gives
+ * the same bits every time.
+ *   q, out: bf16 [tokens][q_heads][head_dim], head_dim contiguous, the other
+ *     strides multiples of 8 elements, bases 16-byte aligned; lse: fp32
+ *     [tokens][q_heads] contiguous or NULL.  Rows that no request has are left as
+ *     they were.  out must not overlap q or the pages.
+ *   q_heads a multiple of heads, q_heads / heads at most 64; requests 1..65535,
+ *     tokens * q_heads and width * page_tokens at most 2^31 - 1.
+ *   max_new: the caller's upper bound on any request's n (it chooses kernels
+ *     and the launch; a request past it is not computed: SKV_PAGES_ROWS).
+ * A request with lens < 0 or > width * P, or whose starts do not ascend
+ * within tokens, counts as having no queries (SKV_PAGES_LENGTH).  Where a
+ * table entry that a request needs names no page of the pool, page 0 is read
+ * in its place and that request's results mean nothing (SKV_PAGES_PAGE).
+ * Two-phase sizing: d_work == NULL sets *work_bytes to the need (at least
+ * 256), which depends on the sizes alone, not on device data.  Calls that may
+ * run at the same time need workspaces of their own. */
+typedef struct {
+    uint32_t abi_version;
+    uint32_t requests, tokens, q_heads, width, max_new;
+    uint32_t causal;       /* 0 or 1 */
+    float scale;
+    int64_t table_stride, q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    const void* q;
+    const void* k_pages;
+    const void* v_pages;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* starts;
+    const float* k_scale;
+    const float* v_scale;
+    void* out;
+    float* lse;
+    uint32_t* status;
+} skv_attention;
+int skv_page_attention(const skv_pages* pages, const skv_attention* a, void* d_work, size_t* work_bytes,
+                       hipStream_t stream);
+
+/* Wait for the stream and look at a status word: SKV_OK when it is zero,
+ * SKV_ERR_PAGES otherwise, *flags (may be NULL) = the word. */
+int skv_page_check(const uint32_t* d_status, uint32_t* flags, hipStream_t stream);
 
 /* Release a library-owned blob and its device copies.  NULL is a no-op. */
 void skv_free(void* tables_blob);

@@ -44,7 +44,8 @@ def build(verbose: bool = False) -> str:
     os.makedirs(out_dir, exist_ok=True)
     objs = []
     for src, device in (("skv_fit.cpp", False), ("skv_api.cpp", False), ("skv_store.cpp", False),
-                        ("skv_kernels.hip", True)):
+                        ("skv_pages.cpp", False), ("skv_kernels.hip", True), ("skv_pages.hip", True),
+                        ("skv_attention.hip", True)):
         obj = os.path.join(out_dir, src + ".o")
         cmd = [hipcc, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
         if device:

@@ -163,6 +163,7 @@ const char* skv_strerror(int status) {
         case SKV_ERR_DEVICE: return "HIP runtime error";
         case SKV_ERR_NOMEM: return "out of memory";
         case SKV_ERR_BUSY: return "store entry in use";
+        case SKV_ERR_PAGES: return "length, page or slot out of range";
         default: return "unknown status";
     }
 }

@@ -7,9 +7,11 @@ kernels. There is no CPU fallback: a missing library or GPU raises.
 from __future__ import annotations
 
 import atexit
+import collections
 import ctypes
 import hashlib
 import os
+import struct
 import sys
 import weakref
 
@@ -23,7 +25,7 @@ ABI_VERSION = 1
 BF16, E4M3, INT16 = 1, 2, 3
 RESIDUAL, CHECKERBOARD, RESIDUAL_EXP, CHECKERBOARD_MAP = 0, 1, 2, 3
 OK, ERR_ARG, ERR_SHAPE, ERR_CAPACITY, ERR_CORRUPT, ERR_TABLES, ERR_DEVICE, ERR_NOMEM = 0, -1, -2, -3, -4, -5, -6, -7
-ERR_BUSY = -8
+ERR_BUSY, ERR_PAGES = -8, -9
 BLOCK_TOKENS = 128
 
 
@@ -121,6 +123,16 @@ def lib():
         L.skv_store_stats.argtypes = [vp, ctypes.POINTER(StoreInfo)]
         L.skv_kernel_times.restype = ctypes.c_int
         L.skv_kernel_times.argtypes = [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_float), ctypes.c_int]
+        i64, i32p = ctypes.c_int64, vp
+        L.skv_page_plan.restype = ctypes.c_int
+        L.skv_page_plan.argtypes = [i32p, i32p, u32, i32p, u32, i64, i32p, u32, u32, u32, i32p, i32p, i32p, i32p, vp, vp]
+        for f in (L.skv_page_write, L.skv_page_read):
+            f.restype = ctypes.c_int
+            f.argtypes = [ctypes.c_char_p, vp, vp, ctypes.c_char_p, vp, vp, i32p, vp, vp, vp, vp]
+        L.skv_page_attention.restype = ctypes.c_int
+        L.skv_page_attention.argtypes = [ctypes.c_char_p, ctypes.c_char_p, vp, psz, vp]
+        L.skv_page_check.restype = ctypes.c_int
+        L.skv_page_check.argtypes = [vp, ctypes.POINTER(u32), vp]
         if L.skv_version() != ABI_VERSION:
             raise RuntimeError("libskv ABI version mismatch")
         _lib = L
@@ -728,3 +740,320 @@ class Store:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------------ paged caches
+PAGES_LENGTH, PAGES_PAGE, PAGES_SLOT, PAGES_FREE, PAGES_ROWS = 1, 2, 4, 8, 16
+PagePlan = collections.namedtuple("PagePlan", "slots positions starts taken")
+
+# The C structs skv_pages, skv_rows and skv_attention, packed field by field.
+_PAGES, _ROWS, _ATTENTION = struct.Struct("8I4q"), struct.Struct("2I3q"), struct.Struct("7If5q11Q")
+_PAGE_TYPES = {torch.bfloat16: BF16, torch.int16: BF16, torch.float8_e4m3fn: E4M3, torch.uint8: E4M3}
+
+
+def _queue(device: torch.device, call, *args) -> int:
+    """call(*args, stream) on the device's current stream, with the device current."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        return call(*args, torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(i):
+        return call(*args, torch.cuda.current_stream().cuda_stream)
+
+
+def _int32(t, name: str, shape: tuple, device) -> int:
+    """Address of a contiguous int32 device tensor of the given shape (None: any size)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != len(shape) or
+            any(w is not None and n != w for n, w in zip(t.shape, shape))):
+        raise ValueError(f"{name} must be an int32 device tensor of shape {shape}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return _dev(t, name)
+
+
+def _table(t, requests: int, device) -> tuple[int, int, int]:
+    """(address, width, row stride) of a block table."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != requests:
+        raise ValueError(f"table must be an int32 device tensor [{requests}][blocks]")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"table must be on {device}")
+    width, stride = t.shape[1], t.stride(0)
+    if (width > 1 and t.stride(1) != 1) or (requests > 1 and stride < width):
+        raise ValueError("table rows must be contiguous and apart")
+    return t.data_ptr(), width, stride
+
+
+def _scale_arg(t, name: str, heads: int, device) -> int:
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or tuple(t.shape) != (heads,):
+        raise ValueError(f"{name} must be a float32 device tensor [{heads}]")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return _dev(t, name)
+
+
+def _status_arg(t, device) -> int:
+    return 0 if t is None else _int32(t, "status", (1,), device)
+
+
+def _strides(t: torch.Tensor, name: str, written: bool) -> list:
+    """Strides, 0 for dimensions of one element; the last one must be 1."""
+    st = [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
+    if t.shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: head_dim must be contiguous")
+    if written and any(s == 0 and n > 1 for n, s in zip(t.shape, st)):
+        raise ValueError(f"{name} is written to and must not be an expanded tensor")
+    return st
+
+
+def _kv_pair(k, v, name: str, dims: tuple, written: bool) -> tuple[int, list]:
+    """(dtype code, strides) of two device tensors of one shape, type and strides."""
+    for t in (k, v):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() not in dims:
+            raise ValueError(f"k_{name} and v_{name} must be device tensors of {' or '.join(map(str, dims))} dimensions")
+    code = _PAGE_TYPES.get(k.dtype)
+    if code is None or v.dtype is not k.dtype or v.shape != k.shape or v.device != k.device:
+        raise ValueError(f"k_{name} and v_{name}: one shape, device and type (bfloat16 or int16, float8_e4m3fn or uint8)")
+    st = _strides(k, "k_" + name, written)
+    if st != _strides(v, "v_" + name, written):
+        raise ValueError(f"k_{name} and v_{name} must have the same strides")
+    return code, st
+
+
+def _pool(k_pages, v_pages, written: bool, dims: tuple = (4, 5)) -> tuple[bytes, int, torch.Size, int]:
+    """(packed skv_pages, dtype code, shape, layers) of a pool of pages."""
+    code, st = _kv_pair(k_pages, v_pages, "pages", dims, written)
+    shape = k_pages.shape
+    layers = shape[0] if len(shape) == 5 else 1
+    pages, page_tokens, heads, dim = shape[-4:]
+    return (_PAGES.pack(ABI_VERSION, code, layers, pages, page_tokens, heads, dim, 0,
+                        st[0] if len(st) == 5 else 0, st[-4], st[-3], st[-2]), code, shape, layers)
+
+
+def page_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: torch.Tensor | None, page_tokens: int,
+              tokens: int, *, out: PagePlan | None = None, status: torch.Tensor | None = None) -> PagePlan:
+    """Block tables and slot maps of a step from request lengths (see
+    skv_page_plan).  lens, new: int32 [requests], a request's tokens after the
+    step and how many of them are new; table: int32 [requests][blocks], updated
+    in place with pages from the int32 list `free` (None: only read, for
+    tokens that have their pages); tokens: packed rows to lay out.  Returns
+    slots and positions [tokens] (-1 behind the last request's rows), starts
+    and taken [requests + 1]; taken[-1] pages of the list are then in use."""
+    if not isinstance(lens, torch.Tensor) or lens.dim() != 1 or not lens.is_cuda:
+        raise ValueError("lens must be an int32 device tensor [requests]")
+    device, n = lens.device, lens.shape[0]
+    pl, pn = _int32(lens, "lens", (None,), device), _int32(new, "new", (n,), device)
+    pt, width, stride = _table(table, n, device)
+    pf, nf = (0, 0) if free is None else (_int32(free, "free", (None,), device), free.shape[0])
+    # an empty list is still a list, whose address torch gives as 0
+    if free is not None and nf == 0:
+        pf = pl
+    if not 0 <= tokens < 1 << 31:
+        raise ValueError("tokens must be 0 .. 2^31 - 1")
+    if out is None:
+        rows = torch.empty((2, tokens), dtype=torch.int32, device=device)
+        sums = torch.empty((2, n + 1), dtype=torch.int32, device=device)
+        out = PagePlan(rows[0], rows[1], sums[0], sums[1])
+    args = (_int32(out.slots, "slots", (tokens,), device), _int32(out.positions, "positions", (tokens,), device),
+            _int32(out.starts, "starts", (n + 1,), device), _int32(out.taken, "taken", (n + 1,), device))
+    _check(_queue(device, lib().skv_page_plan, pl, pn, n, pt, width, stride, pf, nf, page_tokens, tokens, *args,
+                  _status_arg(status, device)), "skv_page_plan")
+    return out
+
+
+def _rows_call(call, what, k, v, k_pages, v_pages, slots, k_scale, v_scale, status, to_pages: bool):
+    desc, code, shape, layers = _pool(k_pages, v_pages, to_pages)
+    rcode, st = _kv_pair(k, v, "rows", (len(shape) - 1,), not to_pages)
+    if k.shape[-2:] != shape[-2:] or (len(shape) == 5 and k.shape[0] != layers):
+        raise ValueError(f"rows {tuple(k.shape)} do not fit pages {tuple(shape)}")
+    device, tokens = k.device, k.shape[-3]
+    if k_pages.device != device:
+        raise ValueError("rows and pages must be on one device")
+    rows = _ROWS.pack(rcode, tokens, st[0] if len(shape) == 5 else 0, st[-3], st[-2])
+    ps = _int32(slots, "slots", (tokens,), device)
+    heads = shape[-2]
+    _check(_queue(device, call, desc, k_pages.data_ptr(), v_pages.data_ptr(), rows, k.data_ptr(), v.data_ptr(), ps,
+                  _scale_arg(k_scale, "k_scale", heads, device), _scale_arg(v_scale, "v_scale", heads, device),
+                  _status_arg(status, device)), what)
+
+
+def page_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor,
+               k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, *,
+               status: torch.Tensor | None = None) -> None:
+    """Rows k, v [tokens][heads][head_dim] into pages [pages][page_tokens]
+    [heads][head_dim] at int32 slots [tokens] (see skv_page_write), or both
+    with a leading dimension of layers.  Any strides that are multiples of 16
+    bytes with head_dim contiguous.  bf16 rows may go into e4m3 pages, divided
+    by the float32 [heads] scales (None: 1)."""
+    _rows_call(lib().skv_page_write, "skv_page_write", k, v, k_pages, v_pages, slots, k_scale, v_scale, status, True)
+
+
+def page_read(k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype | None = None,
+              k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, *, out=None,
+              status: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Rows out of pages (see skv_page_read): k, v [tokens][heads][head_dim]
+    (or with the pages' leading dimension of layers) of `dtype` (None: the
+    pages' own type; e4m3 pages may be read as bfloat16), or into out = (k, v)."""
+    if out is None:
+        if not isinstance(k_pages, torch.Tensor) or k_pages.dim() not in (4, 5) or not isinstance(slots, torch.Tensor):
+            raise ValueError("k_pages must be a device tensor of 4 or 5 dimensions and slots one of int32")
+        lead = (k_pages.shape[0],) if k_pages.dim() == 5 else ()
+        shape = (*lead, slots.numel(), *k_pages.shape[-2:])
+        dt = k_pages.dtype if dtype is None else dtype
+        out = tuple(torch.empty(shape, dtype=dt, device=k_pages.device) for _ in range(2))
+    elif dtype is not None and any(t.dtype is not dtype for t in out):
+        raise ValueError("out is not of the dtype asked for")
+    k, v = out
+    _rows_call(lib().skv_page_read, "skv_page_read", k, v, k_pages, v_pages, slots, k_scale, v_scale, status, False)
+    return k, v
+
+
+def page_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor,
+                   lens: torch.Tensor, starts: torch.Tensor | None = None, max_new: int | None = None, *,
+                   scale: float | None = None, causal: bool = True, k_scale: torch.Tensor | None = None,
+                   v_scale: torch.Tensor | None = None, lse=False, out: torch.Tensor | None = None,
+                   work: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    """Attention of new tokens over pages (see skv_page_attention).  q: bf16
+    [tokens][q_heads][head_dim], the requests' new tokens packed one after
+    another; pages [pages][page_tokens][heads][head_dim] bf16 or e4m3; table,
+    lens: block table and lengths including the new tokens; starts: int32
+    [requests + 1] first rows (None: one row per request); max_new: an upper
+    bound on a request's new tokens (None: tokens).  scale: 1 / sqrt(head_dim)
+    when None.  Returns out like q, or (out, lse) with lse=True or an fp32
+    [tokens][q_heads] tensor to fill.  Rows of no request are left as they
+    were in `out` and lse.  work: a uint8 workspace of at least
+    page_attention_workspace(...) bytes to use in place of one from torch's
+    allocator; it must not be in use by another call at the same time."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype is not torch.bfloat16 or not q.is_cuda:
+        raise ValueError("q must be a bfloat16 device tensor [tokens][q_heads][head_dim]")
+    desc, code, shape, _ = _pool(k_pages, v_pages, False, (4,))
+    device = q.device
+    tokens, q_heads, dim = q.shape
+    heads = shape[2]
+    if k_pages.device != device:
+        raise ValueError("q and pages must be on one device")
+    if dim != shape[3]:
+        raise ValueError(f"q has head_dim {dim}, the pages {shape[3]}")
+    if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
+        raise ValueError("lens must be an int32 device tensor [requests]")
+    n = lens.shape[0]
+    pl = _int32(lens, "lens", (None,), device)
+    ps = 0 if starts is None else _int32(starts, "starts", (n + 1,), device)
+    pt, width, stride = _table(table, n, device)
+    if starts is None and tokens != n:
+        raise ValueError("without starts there is one row per request")
+    if out is None:
+        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=device)
+    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or out.device != device:
+        raise ValueError("out must be like q")
+    if lse is True:
+        lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=device)
+    elif lse is False or lse is None:
+        lse = None
+    elif (lse.dtype is not torch.float32 or lse.shape != (tokens, q_heads) or lse.device != device or
+          not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 tensor [tokens][q_heads]")
+    qs, os_ = _strides(q, "q", False), _strides(out, "out", True)
+    most = tokens if max_new is None else max_new
+    if not 0 <= most < 1 << 32:
+        raise ValueError("max_new must be 0 .. 2^32 - 1")
+    args = _ATTENTION.pack(ABI_VERSION, n, tokens, q_heads, width, most, 1 if causal else 0,
+                           dim ** -0.5 if scale is None else scale, stride, qs[0], qs[1], os_[0], os_[1],
+                           q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pt, pl, ps,
+                           _scale_arg(k_scale, "k_scale", heads, device), _scale_arg(v_scale, "v_scale", heads, device),
+                           out.data_ptr(), 0 if lse is None else lse.data_ptr(), _status_arg(status, device))
+    need = ctypes.c_size_t()
+    _check(lib().skv_page_attention(desc, args, None, ctypes.byref(need), None), "skv_page_attention(size query)")
+    if work is None:
+        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+    elif work.dtype is not torch.uint8 or work.device != device:
+        raise ValueError(f"work must be a uint8 tensor on {device}")
+    size = ctypes.c_size_t(work.numel())
+    _check(_queue(device, lib().skv_page_attention, desc, args, _dev(work, "work"), ctypes.byref(size)),
+           "skv_page_attention")
+    return out if lse is None else (out, lse)
+
+
+def page_check(status: torch.Tensor) -> None:
+    """Wait for the current stream and raise SkvError(ERR_PAGES), with the
+    PAGES_* flags as its `flags`, if a call recorded one in the int32 [1] status."""
+    flags = ctypes.c_uint32()
+    rc = _queue(status.device, lib().skv_page_check, _status_arg(status, status.device), ctypes.byref(flags))
+    if rc != OK:
+        e = SkvError(rc, f"skv_page_check (flags {flags.value})")
+        e.flags = flags.value
+        raise e
+
+
+class PageCache:
+    """A model's cache in pages, [layers][K|V][pages][page_tokens][heads]
+    [head_dim] bf16 or e4m3 codes, with the calls on it: a step plans, writes
+    each layer's new rows and attends; a prefix kept in a Store is restored
+    into pages, and a request's pages are saved into a Store.  Each layer of an
+    e4m3 cache may have scales per head (float32 [layers][heads]).  Flags of
+    all calls gather in `status` (see check)."""
+
+    def __init__(self, dtype: int, layers: int, pages: int, page_tokens: int, heads: int, head_dim: int, device=None,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        if dtype not in (BF16, E4M3):
+            raise ValueError("a paged cache holds BF16 or E4M3 elements")
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and (dtype != E4M3 or tuple(t.shape) != (layers, heads)):
+                raise ValueError(f"{name} belongs to e4m3 pages, float32 [layers][heads]")
+        self.dtype, self.page_tokens, self.k_scale, self.v_scale = dtype, page_tokens, k_scale, v_scale
+        self.data = torch.empty((layers, 2, pages, page_tokens, heads, head_dim), device=dev,
+                                dtype=torch.float8_e4m3fn if dtype == E4M3 else torch.bfloat16)
+        self.k, self.v = self.data[:, 0], self.data[:, 1]
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def _scales(self, layer: int) -> tuple:
+        return tuple(None if t is None else t[layer] for t in (self.k_scale, self.v_scale))
+
+    def plan(self, lens, new, table, free, tokens: int, out: PagePlan | None = None) -> PagePlan:
+        """page_plan with this cache's pages."""
+        return page_plan(lens, new, table, free, self.page_tokens, tokens, out=out, status=self.status)
+
+    def write(self, layer: int, k, v, slots) -> None:
+        """A layer's new rows into its pages (bf16 rows, or the cache's own type)."""
+        scales = self._scales(layer) if _PAGE_TYPES.get(k.dtype) != self.dtype else (None, None)
+        page_write(k, v, self.k[layer], self.v[layer], slots, *scales, status=self.status)
+
+    def attend(self, layer: int, q, table, lens, starts=None, max_new: int | None = None, **kw):
+        """page_attention over a layer's pages."""
+        ks, vs = self._scales(layer)
+        return page_attention(q, self.k[layer], self.v[layer], table, lens, starts, max_new, k_scale=ks, v_scale=vs,
+                              status=self.status, **kw)
+
+    def _as_rows(self, tables: Tables, array: torch.Tensor) -> tuple:
+        """K and V of a codec array [layers][2][tokens][channels] as rows of heads."""
+        layers, _, _, _, heads, dim = self.data.shape
+        if (is_checkerboard(tables.mode) or tables.dtype != self.dtype or tables.layers != layers or tables.kv != 2 or
+                tables.channels != heads * dim or array.dim() != 4):
+            raise ValueError("the tables code a cache of another type or shape than the pages hold")
+        rows = array.view(layers, 2, array.shape[2], heads, dim)
+        return rows[:, 0], rows[:, 1]
+
+    def restore(self, store: "Store", tables: Tables, entry: int, aux: torch.Tensor, slots: torch.Tensor,
+                token_begin: int = 0, token_end: int = 0) -> None:
+        """Decode tokens [token_begin, token_end) of a store's entry (0: all of
+        it) against their predictor aux and put them into the pages at `slots`
+        (one per decoded token), every layer in one pass."""
+        self._as_rows(tables, aux)
+        array = store.decode(tables, entry, aux, token_begin, token_end)
+        k, v = self._as_rows(tables, array)
+        page_write(k, v, self.k.view(k.dtype), self.v.view(k.dtype), slots, status=self.status)
+
+    def save(self, store: "Store", tables: Tables, slots: torch.Tensor, aux: torch.Tensor, hashes) -> tuple[int, int]:
+        """Gather the tokens at `slots` (whole 128-token blocks) from every
+        layer's pages and put them into a store, coded against their predictor
+        aux; returns (entry id, container bytes)."""
+        self._as_rows(tables, aux)
+        array = torch.empty_like(aux)
+        k, v = self._as_rows(tables, array)
+        page_read(self.k.view(k.dtype), self.v.view(k.dtype), slots, out=(k, v), status=self.status)
+        return store.put(tables, array, aux, hashes)
+
+    def check(self) -> None:
+        """Raise SkvError(ERR_PAGES) if any call so far met a length, page or slot out of range."""
+        page_check(self.status)

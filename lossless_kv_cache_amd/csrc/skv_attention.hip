@@ -3,12 +3,21 @@
 // s_j = scale q.k_j over the keys a query sees, m = max s, l = sum exp(s - m),
 // out = sum exp(s - m) v / l, lse = m + log l; in one pass over the keys with
 // a running m and l, o and l rescaled by exp(m_old - m_new) when m grows.
+//
+//   attention_split    requests with at most 32 query rows (new tokens x the
+//                      heads of a KV head): bound by reading the cache, so
+//                      the keys are dealt out evenly over the chip
+//   attention_combine  joins the parts of a request whose keys fell to more
+//                      than one workgroup
+#include <algorithm>
+
 #include "skv_pages.h"
 
 namespace skv {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float bf16_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
@@ -79,32 +88,596 @@ __device__ __forceinline__ void row_plain(const AttentionLaunch& a, uint32_t b, 
     if (a.lse && lane == 0) a.lse[uint64_t(s.row + i) * a.heads * a.group + head] = last < 0 ? -INFINITY : m + __logf(l);
 }
 
+// ------------------------------------------------------------------ tiles
+// Products run on 32x32x16 bf16 MFMA.  Scores are computed transposed, S^T =
+// K Q^T: A = 32 keys x 16 dims, B = 16 dims x 32 query rows, so each lane
+// owns one query row (lane % 32) and 16 of a tile's 32 keys, keys
+//   8 (r / 4) + 4 (lane / 32) + r % 4        (accumulator register r)
+// and row maxima and sums need one exchange between the two half-waves.  The
+// probabilities then are, in place, the B operand of O^T = V^T P^T when V's
+// keys are taken in the same order: the lane's 8 keys of k-step s are
+// registers 8 (s % 2) .. of tile s / 2.  V^T comes from the row-major tile in
+// LDS through the transposing LDS reads.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+#define SKV_LDS(T) __attribute__((address_space(3))) T*
+
+// Geometry of tiles of head_dim D in LDS: rows of RB bytes, 16-byte chunk c
+// of row r kept at chunk c ^ swizzle(r), so that the lanes that read LDS in
+// one cycle (16 of 16 bytes for K, 32 of 8 bytes for V) meet different banks.
+template <int D, bool kE4m3>
+struct Tile {
+    static constexpr int kRow = D * (kE4m3 ? 1 : 2);        // bytes
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kPer256 = kRow >= 256 ? 1 : 256 / kRow;
+    static constexpr int kRowsPerLoad = 1024 / kRow;        // rows that a wave's 16-byte load covers
+    __device__ static uint32_t swizzle_k(uint32_t r) { return (r / kPer256) & (kChunks < 16 ? kChunks - 1 : 15); }
+    __device__ static uint32_t swizzle_v(uint32_t r) {
+        if (!kE4m3) return kRow >= 256 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
+        if (kRow >= 256) return (r & 3) << 1 | (r & 8);
+        if (kRow == 128) return ((r >> 1) & 1) << 1 | ((r >> 1) & 4);
+        return (r >> 2) & 2;
+    }
+};
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((SKV_LDS(const void))p));
+}
+
+// 16 bytes per lane from global memory to LDS at `lds` + 16 * lane, without
+// passing through registers.  The wave waits for it itself (wait_loads).
+// Written as assembly because the compiler would make every later LDS read
+// wait for every such load; no register is written, so nothing can be reused
+// too early.
+__device__ __forceinline__ void load_lds16(const uint8_t* g, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory");
+}
+// Every load above has landed and every LDS read before has its data.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+// Eight e4m3 codes to bf16 (exact: 4 significant bits into 8).
+__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
+    union {
+        bf16x2 h[4];
+        bf16x8 v;
+    } u;
+    u.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return u.v;
+}
+
+// The two k-steps 2p, 2p + 1 of K's A operand for 32 keys from row0: dims 32p
+// .. 32p + 31.  bf16: two 16-byte reads, lane half h holds dims 16s + 8h..;
+// e4m3: one 16-byte read, dims 32p + 16h .. + 15, the first 8 for step 2p (Q
+// is loaded to match, see load_q).
+template <int D, bool kE4m3>
+__device__ __forceinline__ void read_k(const uint8_t* tile, uint32_t row0, int p, uint32_t lane, bf16x8 (&k)[2]) {
+    using T = Tile<D, kE4m3>;
+    const uint32_t r = row0 + (lane & 31), h = lane >> 5, sw = T::swizzle_k(r);
+    if constexpr (!kE4m3) {
+        for (int i = 0; i < 2; ++i)
+            k[i] = *reinterpret_cast<const bf16x8*>(tile + r * T::kRow + (((4 * p + 2 * i + h) ^ sw) << 4));
+    } else {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(tile + r * T::kRow + (((2 * p + h) ^ sw) << 4));
+        k[0] = widen(x[0], x[1]);
+        k[1] = widen(x[2], x[3]);
+    }
+}
+
+// V^T's A operand: dims 32 dt + lane % 32, the 8 keys of the lane's half of
+// the 16 keys from row0 (see above for their order).
+template <int D, bool kE4m3>
+__device__ __forceinline__ bf16x8 read_v(const uint8_t* tile, uint32_t row0, int dt, uint32_t lane) {
+    using T = Tile<D, kE4m3>;
+    const uint32_t h = lane >> 5, side = (lane >> 4) & 1, i = lane & 15;
+    if constexpr (!kE4m3) {
+        union {
+            s16x4 q[2];
+            bf16x8 v;
+        } u;
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t r = row0 + 8 * e + 4 * h + (i >> 2);
+            const uint32_t byte = 64 * dt + 32 * side + 8 * (i & 3);
+            const uint8_t* at = tile + r * T::kRow + ((((byte >> 4) ^ T::swizzle_v(r)) << 4) | (byte & 8));
+            u.q[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SKV_LDS(s16x4))at);
+        }
+        return u.v;
+    } else {
+        const uint32_t j = i >> 1, r = row0 + 4 * h + (j & 3) + 2 * (j & 4);
+        const uint32_t c = 2 * dt + side;
+        const uint8_t* at = tile + r * T::kRow + (((c ^ T::swizzle_v(r)) << 4) | 8 * (i & 1));
+        const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((SKV_LDS(i32x2))at);
+        return widen(uint32_t(x[0]), uint32_t(x[1]));
+    }
+}
+
+// Q^T's B operand for one query row per lane; zero where there is none.  A
+// negative scale is folded into Q's sign (exact), a zero one into Q itself,
+// so the kernels see a positive factor.
+template <int D, bool kE4m3>
+__device__ __forceinline__ void load_q(const uint16_t* row, bool have, float factor, uint32_t lane, bf16x8 (&q)[D / 16]) {
+    const uint32_t h = lane >> 5, flip = factor < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+        union {
+            u32x4 w;
+            bf16x8 v;
+        } u;
+        u.w = u32x4{0, 0, 0, 0};
+        const uint32_t dim = kE4m3 ? 32 * (s >> 1) + 16 * h + 8 * (s & 1) : 16 * s + 8 * h;
+        if (have && factor != 0.0f) u.w = *reinterpret_cast<const u32x4*>(row + dim);
+        u.w ^= flip;
+        q[s] = u.v;
+    }
+}
+
+__device__ __forceinline__ float half_max(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// A wave's running state for 32 query rows: m in units of the raw scores.
+template <int D>
+struct Rows {
+    f32x16 o[D / 32];
+    float m, l;
+    __device__ void clear() {
+        for (auto& t : o)
+            for (int r = 0; r < 16; ++r) t[r] = 0.0f;
+        m = -INFINITY;
+        l = 0.0f;
+    }
+};
+
+// One tile of 32 * NM keys: scores, masked where key > `limit` (relative to
+// the tile; the lane's own row), the running maximum, probabilities, and
+// their product with V.  factor > 0: scale in base-2 units.
+template <int D, bool kE4m3, int NM, bool kMask>
+__device__ __forceinline__ void tile_step(const uint8_t* kt, const uint8_t* vt, const bf16x8 (&q)[D / 16], float factor,
+                                          int limit, uint32_t lane, Rows<D>& st) {
+    f32x16 s[NM];
+#pragma unroll
+    for (int t = 0; t < NM; ++t) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+#pragma unroll
+        for (int p = 0; p < D / 32; ++p) {
+            bf16x8 k[2];
+            read_k<D, kE4m3>(kt, 32 * t, p, lane, k);
+            s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[0], q[2 * p], s[t], 0, 0, 0);
+            s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[1], q[2 * p + 1], s[t], 0, 0, 0);
+        }
+    }
+    if (kMask) {
+        const int lim = limit - 4 * int(lane >> 5);
+#pragma unroll
+        for (int t = 0; t < NM; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (32 * t + 8 * (r / 4) + r % 4 > lim) s[t][r] = -INFINITY;
+    }
+    float top = st.m;
+#pragma unroll
+    for (int t = 0; t < NM; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
+    top = half_max(top);
+    // -infinity stands for "nothing yet" and must not meet itself in a difference
+    const float ref = top == -INFINITY ? 0.0f : top * factor;
+    if (__any(top != st.m)) {
+        const float keep = __builtin_amdgcn_exp2f(fmaf(st.m, factor, -ref));
+        st.l *= keep;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) st.o[t][r] *= keep;
+        st.m = top;
+    }
+#pragma unroll
+    for (int t = 0; t < NM; ++t) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            union {
+                bf16x2 h[4];
+                bf16x8 v;
+            } p;
+#pragma unroll
+            for (int r = 0; r < 8; r += 2) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[t][8 * hf + r], factor, -ref));
+                const float y = __builtin_amdgcn_exp2f(fmaf(s[t][8 * hf + r + 1], factor, -ref));
+                st.l += x + y;
+                // rounded to the MFMA's operand type: each probability by at most half a step of bf16, as the
+                // result itself is; the sum keeps them in 32 bits
+                p.h[r / 2] = bf16x2{__bf16(x), __bf16(y)};
+            }
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+                st.o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v<D, kE4m3>(vt, 32 * t + 16 * hf, dt, lane), p.v,
+                                                                   st.o[dt], 0, 0, 0);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ few rows
+// The keys of every (request, KV head) are cut into units of kWaves * kKeys
+// tokens, all units numbered through, and each of kParts workgroups takes an
+// equal run of them: the cache is read once and evenly however different the
+// lengths are.  A workgroup's run covers whole (request, head)s, which it
+// finishes, and at most two broken ones (its first and last), whose
+// unnormalized sums go to the workspace for attention_combine.
+//
+// A wave keeps two tiles of 16 KB in LDS of its own: one being used, the
+// other on its way straight from memory, 64 KB in flight per CU.
+constexpr uint32_t kSplitRows = 32;
+
+template <int D, bool kE4m3>
+struct Split {
+    static constexpr int kWaves = D == 256 && !kE4m3 ? 2 : 4;
+    static constexpr int kStage = kWaves == 2 ? 32768 : 16384;             // bytes of K and V per wave
+    static constexpr int kKeys = kStage / 2 / Tile<D, kE4m3>::kRow;         // per wave and tile
+    static constexpr int kUnit = kWaves * kKeys;
+};
+
+constexpr uint32_t kParts = 256;      // one workgroup per CU (128 KB of LDS)
+
+struct Units {
+    uint64_t total;                   // units of the whole batch
+    uint64_t first;                   // of the request looked for
+    uint32_t request;
+};
+
+// Units of one head of request b: at least one where it has queries at all,
+// so that rows that see no key get their zeros.
+__device__ __forceinline__ uint32_t units_of(const AttentionLaunch& a, uint32_t b, uint32_t unit, uint32_t& flags) {
+    const Span s = span_of(a, b, flags);
+    if (s.n == 0 || s.n * a.group > kSplitRows) return 0;
+    return max(1u, (s.len + unit - 1) / unit);
+}
+
+// Sum over the workgroup's threads of x (kThreads of them), to all.
+template <int kThreads>
+__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* s_wave, uint64_t* total) {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (uint32_t d = 1; d < 64; d <<= 1) {
+        const uint64_t y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) s_wave[wave] = x;
+    __syncthreads();
+    uint64_t sum = 0;
+    for (uint32_t w = 0; w < kThreads / 64; ++w) {
+        if (w < wave) x += s_wave[w];
+        sum += s_wave[w];
+    }
+    *total = sum;
+    return x;                          // inclusive
+}
+
+// The batch's units and, with find(total) naming a unit, the request it
+// belongs to and that request's first unit.  s_out: LDS for the answer.
+template <int kThreads, class Find>
+__device__ Units find_units(const AttentionLaunch& a, uint32_t unit, uint32_t& flags, Find find, uint64_t* s_wave,
+                            uint64_t* s_out) {
+    Units u{0, 0, a.requests};
+    uint64_t mine = 0, total;
+    for (uint32_t b = threadIdx.x; b < a.requests; b += kThreads) mine += units_of(a, b, unit, flags);
+    (void)block_scan<kThreads>(mine, s_wave, &total);
+    u.total = total * a.heads;
+    const uint64_t at = find(u.total);
+    if (at >= u.total) return u;
+    uint64_t before = 0;
+    uint32_t ignore = 0;
+    for (uint32_t base = 0; base < a.requests; base += kThreads) {
+        const uint32_t b = base + threadIdx.x;
+        const uint64_t n = b < a.requests ? units_of(a, b, unit, ignore) : 0;
+        const uint64_t end = before + block_scan<kThreads>(n, s_wave, &total);
+        if (n && at >= (end - n) * a.heads && at < end * a.heads) {
+            s_out[0] = (end - n) * a.heads;
+            s_out[1] = b;
+        }
+        before += total;
+        if (at < before * a.heads) break;
+    }
+    __syncthreads();
+    u.first = s_out[0];
+    u.request = uint32_t(s_out[1]);
+    return u;
+}
+
+// Workgroups with work: every one of them has at least one unit.
+__device__ __forceinline__ uint64_t parts_of(uint64_t total) { return min(total, uint64_t(kParts)); }
+__device__ __forceinline__ uint64_t part_begin(uint64_t total, uint32_t part) {
+    return part < parts_of(total) ? total * part / parts_of(total) : total;
+}
+
+// Workspace: part p's slot: 32 rows of D sums, then 32 maxima (base-2 units)
+// and 32 sums of probabilities.
+template <int D>
+__device__ __forceinline__ float* part_slot(void* work, uint32_t part, uint32_t slot) {
+    return static_cast<float*>(work) + (uint64_t(part) * 2 + slot) * kSplitRows * (D + 2);
+}
+
+__device__ __forceinline__ float exp2_diff(float m, float top) {      // exp2(m - top), 0 for "nothing"
+    return m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+}
+
+// Four values of a finished row to memory; true if one is NaN.
+__device__ __forceinline__ bool store_out(const AttentionLaunch& a, uint64_t row, uint32_t head, uint32_t dim, f32x4 x) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 w;
+    w[0] = bf16_of(x[0]) | bf16_of(x[1]) << 16;
+    w[1] = bf16_of(x[2]) | bf16_of(x[3]) << 16;
+    *reinterpret_cast<u32x2*>(a.out + int64_t(row) * a.out_token + int64_t(head) * a.out_head + dim) = w;
+    return x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3];
+}
+
+__device__ __forceinline__ void store_lse(const AttentionLaunch& a, uint64_t row, uint32_t head, float m, float l) {
+    if (a.lse) a.lse[row * (uint64_t(a.heads) * a.group) + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_split(AttentionLaunch a, void* work) {
+    using G = Split<D, kE4m3>;
+    using T = Tile<D, kE4m3>;
+    constexpr int kThreads = G::kWaves * 64, kLoads = G::kStage / 2 / 1024, kLanes = 64 / T::kRowsPerLoad;
+    __shared__ __align__(1024) uint8_t s_tiles[G::kWaves][2][G::kStage];
+    __shared__ float s_m[G::kWaves][kSplitRows], s_l[G::kWaves][kSplitRows];
+    __shared__ uint64_t s_wave[G::kWaves], s_found[2];
+    __shared__ uint32_t s_bad;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t part = blockIdx.x;
+    uint32_t flags = 0;
+    Units un = find_units<kThreads>(a, G::kUnit, flags, [&](uint64_t total) { return part_begin(total, part); }, s_wave,
+                                    s_found);
+    if (part == 0 && flags && a.status) atomicOr(a.status, flags);
+    uint64_t u = part_begin(un.total, part);
+    const uint64_t begin = u, end = part_begin(un.total, part + 1);
+    if (u >= end) return;
+    flags = 0;
+    uint32_t b = un.request, ignore = 0;
+    uint64_t first = un.first;
+    uint32_t units = units_of(a, b, G::kUnit, ignore);
+    Span sp = span_of(a, b, ignore);
+
+    while (u < end) {
+        // the request and head of unit u, and the run of its units that is ours
+        while (u - first >= uint64_t(units) * a.heads || units == 0) {
+            first += uint64_t(units) * a.heads;
+            if (++b >= a.requests) return;
+            units = units_of(a, b, G::kUnit, ignore);
+            sp = span_of(a, b, ignore);
+        }
+        const uint32_t head = uint32_t((u - first) / units), c0 = uint32_t((u - first) % units);
+        const uint32_t c1 = uint32_t(min(uint64_t(units), c0 + (end - u)));
+        const bool whole = c0 == 0 && c1 == units;
+        const uint32_t rows = sp.n * a.group, row = lane & 31;
+        const uint32_t qi = row / a.group, qg = row - qi * a.group;
+        const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
+        const float raw = a.scale * (a.k_scale ? a.k_scale[head] : 1.0f);
+        const float factor = raw == 0.0f ? 1.0f : fabsf(raw) * kLog2e;
+        bf16x8 q[D / 16];
+        load_q<D, kE4m3>(a.q + int64_t(sp.row + qi) * a.q_token + int64_t(head * a.group + qg) * a.q_head, row < rows,
+                         raw, lane, q);
+        const int first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;     // of query 0
+        const int limit = row < rows ? first_limit + (a.causal ? int(qi) : 0) : -1;
+        Rows<D> st;
+        st.clear();
+
+        const uint8_t* kb = a.k_pages + int64_t(head) * a.head_stride;
+        const uint8_t* vb = a.v_pages + int64_t(head) * a.head_stride;
+        const uint32_t step = G::kUnit;
+        uint32_t t0 = c0 * step + wave * G::kKeys;                       // the tile in use
+        const uint32_t stop = min(c1 * step, sp.len);
+        const uint32_t lds0 = lds_address(&s_tiles[wave][0][0]);
+        // lane j looks up token j of a tile (and j + 64 where tiles are that long)
+        constexpr int kLook = G::kKeys > 64 ? 2 : 1;
+        auto look_up = [&](uint32_t at, int32_t (&e)[kLook]) {
+            for (int i = 0; i < kLook; ++i)
+                e[i] = a.table[int64_t(b) * a.table_stride + (min(at + 64 * i + lane, sp.len - 1) >> a.page_shift)];
+        };
+        auto load_tile = [&](uint32_t at, const int32_t (&e)[kLook], uint32_t stage) {
+            int64_t off[kLook];
+            for (int i = 0; i < kLook; ++i) {
+                const uint32_t token = min(at + 64 * i + lane, sp.len - 1);
+                bool bad = false;
+                const uint32_t page = page_or_zero(e[i], a.pages, &bad);
+                if (bad) flags |= SKV_PAGES_PAGE;
+                off[i] = int64_t(page) * a.page_stride + int64_t(token & ((1u << a.page_shift) - 1)) * a.token_stride;
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const uint32_t r = i * T::kRowsPerLoad + lane / kLanes, c = lane % kLanes;
+                const int64_t o = __shfl(off[(i * T::kRowsPerLoad) / 64], int(r & 63));
+                load_lds16(kb + o + ((c ^ T::swizzle_k(r)) << 4), lds0 + stage * G::kStage + i * 1024);
+                load_lds16(vb + o + ((c ^ T::swizzle_v(r)) << 4), lds0 + stage * G::kStage + G::kStage / 2 + i * 1024);
+            }
+        };
+        if (t0 < stop) {
+            int32_t e[kLook];
+            look_up(t0, e);
+            int32_t next[kLook];
+            look_up(t0 + step, next);
+            load_tile(t0, e, 0);
+            for (uint32_t stage = 0; t0 < stop; t0 += step, stage ^= 1) {
+                wait_loads();
+                if (t0 + step < stop) {
+                    for (int i = 0; i < kLook; ++i) e[i] = next[i];
+                    look_up(t0 + 2 * step, next);
+                    load_tile(t0 + step, e, stage ^ 1);
+                }
+                const uint8_t* kt = &s_tiles[wave][stage][0];
+                if (int(t0) + G::kKeys - 1 > first_limit)
+                    tile_step<D, kE4m3, G::kKeys / 32, true>(kt, kt + G::kStage / 2, q, factor, limit - int(t0), lane, st);
+                else
+                    tile_step<D, kE4m3, G::kKeys / 32, false>(kt, kt + G::kStage / 2, q, factor, 0, lane, st);
+            }
+        }
+        // join the waves: sums to LDS (each into its own tiles), then every thread takes some of a row's values
+        wait_loads();
+        if (row < rows) {
+            f32x4* mine = reinterpret_cast<f32x4*>(&s_tiles[wave][0][0]) + row * (D / 4);
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    mine[(8 * t + 2 * (r / 4) + (lane >> 5)) ^ (row & 7)] =
+                        f32x4{st.o[t][r], st.o[t][r + 1], st.o[t][r + 2], st.o[t][r + 3]};
+            const float l = half_sum(st.l);
+            if (lane < 32) {
+                s_m[wave][row] = st.m * factor;
+                s_l[wave][row] = l;
+            }
+        }
+        if (tid == 0) s_bad = 0;
+        __syncthreads();
+        float* slot = part_slot<D>(work, part, u != begin);
+        for (uint32_t i = tid; i < rows * (D / 4); i += kThreads) {
+            const uint32_t r = i / (D / 4), f = i % (D / 4);
+            float top = s_m[0][r], l = 0.0f;
+            for (int w = 1; w < G::kWaves; ++w) top = fmaxf(top, s_m[w][r]);
+            f32x4 o{0, 0, 0, 0};
+            for (int w = 0; w < G::kWaves; ++w) {
+                const float k = exp2_diff(s_m[w][r], top);
+                l += k * s_l[w][r];
+                o += k * reinterpret_cast<const f32x4*>(&s_tiles[w][0][0])[r * (D / 4) + (f ^ (r & 7))];
+            }
+            if (whole) {
+                const uint32_t ri = r / a.group, qh = head * a.group + r - ri * a.group;
+                const bool none = first_limit + (a.causal ? int(ri) : 0) < 0;
+                const float inv = vs / l;
+                const bool nan = store_out(a, sp.row + ri, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : o * inv);
+                if (nan && a.causal && sp.n > 1) atomicOr(&s_bad, 1u << r);
+                if (f == 0) store_lse(a, sp.row + ri, qh, none ? -INFINITY : top, none ? 1.0f : l);
+            } else {
+                *reinterpret_cast<f32x4*>(slot + r * D + 4 * f) = o;
+                if (f == 0) {
+                    slot[kSplitRows * D + r] = top;
+                    slot[kSplitRows * (D + 1) + r] = l;
+                }
+            }
+        }
+        __syncthreads();
+        // A NaN in a value that only later queries see has reached a row through 0 * NaN in a shared tile: such
+        // rows (and those whose NaN is their own) are computed again, key after key.
+        for (uint32_t r = 0, bad = s_bad; r < rows; ++r)
+            if ((bad >> r & 1) && r % G::kWaves == wave)
+                row_plain<D, kE4m3>(a, b, sp, r / a.group, head * a.group + r % a.group, flags);
+        __syncthreads();
+        u += c1 - c0;
+    }
+    if (flags && a.status) atomicOr(a.status, flags);
+}
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(256) attention_combine(AttentionLaunch a, const void* work) {
+    using G = Split<D, kE4m3>;
+    __shared__ uint64_t s_wave[4];
+    __shared__ uint32_t s_bad;
+    const uint32_t head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    uint32_t flags = 0;
+    const uint32_t units = units_of(a, b, G::kUnit, flags);
+    if (units == 0) return;
+    // this request's first unit: the sum of the earlier ones' units
+    uint64_t before = 0, rest = 0, total;
+    for (uint32_t i = tid; i < a.requests; i += 256) {
+        const uint32_t n = units_of(a, i, G::kUnit, flags);
+        if (i < b) before += n;
+        else rest += n;
+    }
+    (void)block_scan<256>(before, s_wave, &total);
+    before = total;
+    (void)block_scan<256>(rest, s_wave, &total);
+    const uint64_t all = (before + total) * a.heads, u0 = before * a.heads + uint64_t(head) * units, u1 = u0 + units;
+    // the part that has unit u: the last p with all * p / parts <= u
+    const uint32_t p0 = uint32_t(((u0 + 1) * parts_of(all) - 1) / all), p1 = uint32_t((u1 * parts_of(all) - 1) / all);
+    if (p0 == p1) return;              // finished by one workgroup
+    const Span sp = span_of(a, b, flags);
+    const uint32_t rows = sp.n * a.group;
+    const int first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;
+    const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < rows * (D / 4); i += 256) {
+        const uint32_t r = i / (D / 4), f = i % (D / 4);
+        float top = -INFINITY, l = 0.0f;
+        f32x4 o{0, 0, 0, 0};
+        for (uint32_t p = p0; p <= p1; ++p) {
+            const float* slot = part_slot<D>(const_cast<void*>(work), p, part_begin(all, p) < u0);
+            const float m = slot[kSplitRows * D + r], next = fmaxf(top, m);
+            const float keep = exp2_diff(top, next), add = exp2_diff(m, next);
+            l = l * keep + slot[kSplitRows * (D + 1) + r] * add;
+            o = o * keep + *reinterpret_cast<const f32x4*>(slot + r * D + 4 * f) * add;
+            top = next;
+        }
+        const uint32_t ri = r / a.group, qh = head * a.group + r - ri * a.group;
+        const bool none = first_limit + (a.causal ? int(ri) : 0) < 0;
+        const bool nan = store_out(a, sp.row + ri, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : o * (vs / l));
+        if (nan && a.causal && sp.n > 1) atomicOr(&s_bad, 1u << r);
+        if (f == 0) store_lse(a, sp.row + ri, qh, none ? -INFINITY : top, none ? 1.0f : l);
+    }
+    __syncthreads();
+    for (uint32_t r = 0, bad = s_bad; r < rows; ++r)
+        if ((bad >> r & 1) && r % 4 == (tid >> 6))
+            row_plain<D, kE4m3>(a, b, sp, r / a.group, head * a.group + r % a.group, flags);
+}
+
+// ------------------------------------------------------------------ many rows
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(256) attention_rows(AttentionLaunch a) {
     const uint32_t head = blockIdx.y, b = blockIdx.z, i = blockIdx.x * 4 + (threadIdx.x >> 6);
     uint32_t flags = 0;
     const Span s = span_of(a, b, flags);
-    if (i < s.n) row_plain<D, kE4m3>(a, b, s, i, head, flags);
+    if (i < s.n && s.n * a.group > a.least_rows) row_plain<D, kE4m3>(a, b, s, i, head, flags);
     if (flags && a.status) atomicOr(a.status, flags);
 }
 
+// A request's rows decide which kernel computes it; the host knows only the
+// largest number of new tokens, and that a batch as full as it can be has
+// that many in every request.
+bool has_few(const AttentionLaunch& a) {
+    return a.max_new * uint64_t(a.group) <= kSplitRows || uint64_t(a.max_new) * a.requests > a.tokens;
+}
+
 template <int D, bool kE4m3>
-hipError_t launch_rows_kernel(const AttentionLaunch& a, hipStream_t stream) {
-    const dim3 grid((a.max_new + 3) / 4, a.heads * a.group, a.requests);
-    attention_rows<D, kE4m3><<<grid, 256, 0, stream>>>(a);
+hipError_t launch(AttentionLaunch a, void* work, hipStream_t stream) {
+    a.least_rows = has_few(a) ? kSplitRows : 0;
+    if (has_few(a)) {
+        attention_split<D, kE4m3><<<kParts, Split<D, kE4m3>::kWaves * 64, 0, stream>>>(a, work);
+        attention_combine<D, kE4m3><<<dim3(a.heads, a.requests), 256, 0, stream>>>(a, work);
+    }
+    if (a.max_new * uint64_t(a.group) > kSplitRows) {
+        const dim3 grid((a.max_new + 3) / 4, a.heads * a.group, a.requests);
+        attention_rows<D, kE4m3><<<grid, 256, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 
-uint64_t attention_work_bytes(const AttentionLaunch&, uint32_t) { return 256; }
+uint64_t attention_work_bytes(const AttentionLaunch& a, uint32_t head_dim) {
+    return has_few(a) ? uint64_t(kParts) * 2 * kSplitRows * (head_dim + 2) * 4 : 256;
+}
 
-hipError_t launch_attention(const AttentionLaunch& a, uint32_t head_dim, uint32_t dtype, void*, hipStream_t stream) {
+hipError_t launch_attention(const AttentionLaunch& a, uint32_t head_dim, uint32_t dtype, void* work,
+                            hipStream_t stream) {
     const bool e4m3 = dtype == SKV_E4M3;
     switch (head_dim) {
-        case 64: return e4m3 ? launch_rows_kernel<64, true>(a, stream) : launch_rows_kernel<64, false>(a, stream);
-        case 128: return e4m3 ? launch_rows_kernel<128, true>(a, stream) : launch_rows_kernel<128, false>(a, stream);
-        default: return e4m3 ? launch_rows_kernel<256, true>(a, stream) : launch_rows_kernel<256, false>(a, stream);
+        case 64: return e4m3 ? launch<64, true>(a, work, stream) : launch<64, false>(a, work, stream);
+        case 128: return e4m3 ? launch<128, true>(a, work, stream) : launch<128, false>(a, work, stream);
+        default: return e4m3 ? launch<256, true>(a, work, stream) : launch<256, false>(a, work, stream);
     }
 }
 

@@ -312,9 +312,11 @@ def compare(got, want, rows):
     o, to, l, tl = (x[:rows] for x in want)
     assert torch.equal(out.isnan(), o.isnan())
     d = torch.where(o.isnan() | (out == o), 0.0, (out - o).abs())
-    assert bool(((d <= to) | (d == 0)).all()), (d / to).max()          # (where both are NaN, so is the tolerance)
+    ok = bool(((d <= to) | (d == 0)).all())          # (where both are NaN, so is the tolerance)
+    assert ok, f"out is {(d / to).max().item():.3g} times its tolerance off"
     d = torch.where(lse == l, 0.0, (lse - l).abs())
-    assert bool((d <= tl).all()), (d / tl).max()
+    ok = bool((d <= tl).all())
+    assert ok, f"lse is {(d / tl).max().item():.3g} times its tolerance off"
 
 
 LENGTHS = {

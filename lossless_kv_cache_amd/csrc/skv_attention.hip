@@ -9,6 +9,8 @@
 //                      the keys are dealt out evenly over the chip
 //   attention_combine  joins the parts of a request whose keys fell to more
 //                      than one workgroup
+//   attention_tiles    requests with more rows: 128 of them share the keys
+//   attention_tile_combine  joins the runs of keys that few tiles are cut into
 #include <algorithm>
 
 #include "skv_pages.h"
@@ -635,13 +637,218 @@ __global__ void __launch_bounds__(256) attention_combine(AttentionLaunch a, cons
 }
 
 // ------------------------------------------------------------------ many rows
+// A workgroup takes 128 query rows of one (request, KV head): new tokens x
+// the head's query heads, in that order, so all of them share the keys it
+// streams through LDS, 64 at a time, two tiles deep.  Each wave owns 32 rows.
+//
+// Tiles of query rows are numbered so that no sum over requests is needed:
+// request b's first is floor(starts[b] * group / 128) + b, which leaves it at
+// least ceil(n * group / 128) numbers.  The heads come fastest: eight
+// consecutive workgroups go to the eight XCDs, so with 8 KV heads (or a
+// divisor or multiple) each XCD's L2 holds the keys of its own heads.  The
+// last rows, which see the most keys, come first.
+//
+// With few tiles the keys are cut into `splits` runs whose unnormalized sums
+// attention_tile_combine joins.
+constexpr uint32_t kTileRows = 128, kTileKeys = 64;
+
+struct TilePlace {
+    uint32_t request, row;             // request (none: a.requests), first of its rows
+    Span span;
+};
+
+__device__ __forceinline__ TilePlace find_tile(const AttentionLaunch& a, uint32_t tile, uint32_t& flags, uint32_t* s_at) {
+    if (threadIdx.x == 0) *s_at = a.requests;
+    __syncthreads();
+    for (uint32_t b = threadIdx.x; b < a.requests; b += blockDim.x) {
+        const Span s = span_of(a, b, flags);
+        const uint32_t rows = s.n * a.group, first = uint32_t(uint64_t(s.row) * a.group / kTileRows) + b;
+        if (rows > a.least_rows && tile >= first && tile - first < (rows + kTileRows - 1) / kTileRows) *s_at = b;
+    }
+    __syncthreads();
+    TilePlace t{*s_at, 0, Span{0, 0, 0}};
+    if (t.request < a.requests) {
+        uint32_t ignore = 0;
+        t.span = span_of(a, t.request, ignore);
+        t.row = (tile - (uint32_t(uint64_t(t.span.row) * a.group / kTileRows) + t.request)) * kTileRows;
+    }
+    return t;
+}
+
+__host__ __device__ __forceinline__ uint32_t tile_count(const AttentionLaunch& a) {
+    return uint32_t(uint64_t(a.tokens) * a.group / kTileRows) + a.requests;
+}
+
+// Keys that rows up to `row` of a request see.
+__device__ __forceinline__ uint32_t keys_for(const AttentionLaunch& a, const Span& s, uint32_t row) {
+    if (!a.causal) return s.len;
+    const uint32_t rows = s.n * a.group;
+    const int64_t last = int64_t(s.len) - s.n + min(row, rows - 1) / a.group;
+    return last < 0 ? 0 : uint32_t(last) + 1;
+}
+
+template <int D>
+__device__ __forceinline__ float* tile_slot(void* work, uint64_t id) {
+    return static_cast<float*>(work) + id * kTileRows * (D + 2);
+}
+
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(256) attention_rows(AttentionLaunch a) {
-    const uint32_t head = blockIdx.y, b = blockIdx.z, i = blockIdx.x * 4 + (threadIdx.x >> 6);
+struct TileGeo {
+    static constexpr int kStage = 2 * kTileKeys * Tile<D, kE4m3>::kRow;
+    static constexpr int kPerCu = 2 * kStage > 80 * 1024 ? 1 : 2;        // workgroups that fit a CU's LDS
+};
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_tiles(AttentionLaunch a, void* work) {
+    using T = Tile<D, kE4m3>;
+    using G = TileGeo<D, kE4m3>;
+    constexpr int kWaveRows = kTileKeys / 4, kLoads = kWaveRows * T::kRow / 1024, kLanes = 64 / T::kRowsPerLoad;
+    __shared__ __align__(1024) uint8_t s_tiles[2][G::kStage];
+    __shared__ uint32_t s_at;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t head = blockIdx.x % a.heads, tile = tile_count(a) - 1 - blockIdx.x / a.heads, split = blockIdx.y;
     uint32_t flags = 0;
-    const Span s = span_of(a, b, flags);
-    if (i < s.n && s.n * a.group > a.least_rows) row_plain<D, kE4m3>(a, b, s, i, head, flags);
+    const TilePlace place = find_tile(a, tile, flags, &s_at);
+    if (blockIdx.x == 0 && split == 0 && flags && a.status) atomicOr(a.status, flags);
+    flags = 0;
+    if (place.request >= a.requests) return;
+    const uint32_t b = place.request;
+    const Span sp = place.span;
+    const uint32_t rows = sp.n * a.group, row = place.row + 32 * wave + (lane & 31);
+    const uint32_t qi = row / a.group, qg = row - qi * a.group, qh = head * a.group + qg;
+    const bool have = row < rows;
+    const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
+    const float raw = a.scale * (a.k_scale ? a.k_scale[head] : 1.0f);
+    const float factor = raw == 0.0f ? 1.0f : fabsf(raw) * kLog2e;
+    bf16x8 q[D / 16];
+    load_q<D, kE4m3>(a.q + int64_t(sp.row + qi) * a.q_token + int64_t(qh) * a.q_head, have, raw, lane, q);
+    const int first = int(sp.len) - int(sp.n);
+    const int limit = !have ? -1 : a.causal ? first + int(qi) : int(sp.len) - 1;
+    // of the wave's rows: the keys that all of them see, and the keys that any of them sees
+    const uint32_t wave_row = place.row + 32 * wave;
+    const int all_see = wave_row >= rows ? 0 : a.causal ? max(first + int(wave_row / a.group) + 1, 0) : int(sp.len);
+    const int any_sees = wave_row >= rows ? 0 : int(keys_for(a, sp, wave_row + 31));
+    const uint32_t keys = keys_for(a, sp, place.row + kTileRows - 1);
+    const uint32_t tiles = (keys + kTileKeys - 1) / kTileKeys;
+    const uint32_t begin = uint32_t(uint64_t(tiles) * split / gridDim.y) * kTileKeys;
+    const uint32_t end = min(uint32_t(uint64_t(tiles) * (split + 1) / gridDim.y) * kTileKeys, keys);
+    Rows<D> st;
+    st.clear();
+
+    const uint8_t* kb = a.k_pages + int64_t(head) * a.head_stride;
+    const uint8_t* vb = a.v_pages + int64_t(head) * a.head_stride;
+    const uint32_t lds0 = lds_address(&s_tiles[0][0]) + wave * kWaveRows * T::kRow;
+    // a wave brings in 16 of the 64 keys; lane j looks up the j-th of them
+    auto token_of = [&](uint32_t at) { return min(at + wave * kWaveRows + (lane & 15), sp.len - 1); };
+    auto look_up = [&](uint32_t at) { return a.table[int64_t(b) * a.table_stride + (token_of(at) >> a.page_shift)]; };
+    auto load_tile = [&](uint32_t at, int32_t entry, uint32_t stage) {
+        const uint32_t token = token_of(at);
+        bool bad = false;
+        const uint32_t page = page_or_zero(entry, a.pages, &bad);
+        if (bad) flags |= SKV_PAGES_PAGE;
+        const int64_t off = int64_t(page) * a.page_stride + int64_t(token & ((1u << a.page_shift) - 1)) * a.token_stride;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t in = i * T::kRowsPerLoad + lane / kLanes, r = wave * kWaveRows + in, c = lane % kLanes;
+            const int64_t o = __shfl(off, int(in));
+            load_lds16(kb + o + ((c ^ T::swizzle_k(r)) << 4), lds0 + stage * G::kStage + i * 1024);
+            load_lds16(vb + o + ((c ^ T::swizzle_v(r)) << 4), lds0 + stage * G::kStage + G::kStage / 2 + i * 1024);
+        }
+    };
+    if (begin < end) {
+        int32_t entry = look_up(begin), next = look_up(begin + kTileKeys);
+        load_tile(begin, entry, 0);
+        uint32_t stage = 0;
+        for (uint32_t t0 = begin; t0 < end; t0 += kTileKeys, stage ^= 1) {
+            wait_loads();
+            __syncthreads();
+            if (t0 + kTileKeys < end) {
+                entry = next;
+                next = look_up(t0 + 2 * kTileKeys);
+                load_tile(t0 + kTileKeys, entry, stage ^ 1);
+            }
+            const uint8_t* kt = &s_tiles[stage][0];
+            if (int(t0) >= any_sees) continue;
+            if (int(t0 + kTileKeys) > all_see)
+                tile_step<D, kE4m3, kTileKeys / 32, true>(kt, kt + G::kStage / 2, q, factor, limit - int(t0), lane, st);
+            else
+                tile_step<D, kE4m3, kTileKeys / 32, false>(kt, kt + G::kStage / 2, q, factor, 0, lane, st);
+        }
+    }
+    const float l = half_sum(st.l);
+    if (gridDim.y > 1) {
+        float* slot = tile_slot<D>(work, (uint64_t(tile) * a.heads + head) * gridDim.y + split);
+        const uint32_t r0 = 32 * wave + (lane & 31);
+        if (have) {
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<f32x4*>(slot + r0 * D + 32 * t + 2 * r + 4 * (lane >> 5)) =
+                        f32x4{st.o[t][r], st.o[t][r + 1], st.o[t][r + 2], st.o[t][r + 3]};
+            if (lane < 32) {
+                slot[kTileRows * D + r0] = st.m * factor;
+                slot[kTileRows * (D + 1) + r0] = l;
+            }
+        }
+    } else {
+        bool nan = false;
+        if (have) {
+            const bool none = limit < 0;
+            const float inv = none ? 0.0f : vs / l;
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    const f32x4 o{st.o[t][r], st.o[t][r + 1], st.o[t][r + 2], st.o[t][r + 3]};
+                    nan |= store_out(a, sp.row + qi, qh, 32 * t + 2 * r + 4 * (lane >> 5), none ? f32x4{0, 0, 0, 0} : o * inv);
+                }
+            if (lane < 32) store_lse(a, sp.row + qi, qh, none ? -INFINITY : st.m * factor, none ? 1.0f : l);
+        }
+        const uint64_t any = __ballot(nan && a.causal);
+        for (uint32_t bad = uint32_t(any) | uint32_t(any >> 32); bad; bad &= bad - 1) {       // as in attention_split
+            const uint32_t r = wave_row + __builtin_ctz(bad);
+            row_plain<D, kE4m3>(a, b, sp, r / a.group, head * a.group + r % a.group, flags);
+        }
+    }
     if (flags && a.status) atomicOr(a.status, flags);
+}
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(256) attention_tile_combine(AttentionLaunch a, void* work, uint32_t splits) {
+    __shared__ uint32_t s_at, s_bad[4];
+    const uint32_t tid = threadIdx.x, head = blockIdx.x % a.heads, tile = blockIdx.x / a.heads;
+    uint32_t flags = 0;
+    const TilePlace place = find_tile(a, tile, flags, &s_at);
+    if (place.request >= a.requests) return;
+    const Span sp = place.span;
+    const uint32_t rows = min(kTileRows, sp.n * a.group - place.row);
+    const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
+    if (tid < 4) s_bad[tid] = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < rows * (D / 4); i += 256) {
+        const uint32_t r = i / (D / 4), f = i % (D / 4);
+        float top = -INFINITY, l = 0.0f;
+        f32x4 o{0, 0, 0, 0};
+        for (uint32_t p = 0; p < splits; ++p) {
+            const float* slot = tile_slot<D>(work, (uint64_t(tile) * a.heads + head) * splits + p);
+            const float m = slot[kTileRows * D + r], next = fmaxf(top, m);
+            const float keep = exp2_diff(top, next), add = exp2_diff(m, next);
+            l = l * keep + slot[kTileRows * (D + 1) + r] * add;
+            o = o * keep + *reinterpret_cast<const f32x4*>(slot + r * D + 4 * f) * add;
+            top = next;
+        }
+        const uint32_t row = place.row + r, qi = row / a.group, qh = head * a.group + row - qi * a.group;
+        const bool none = keys_for(a, sp, row) == 0;
+        const bool nan = store_out(a, sp.row + qi, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : o * (vs / l));
+        if (nan && a.causal) atomicOr(&s_bad[r >> 5], 1u << (r & 31));
+        if (f == 0) store_lse(a, sp.row + qi, qh, none ? -INFINITY : top, none ? 1.0f : l);
+    }
+    __syncthreads();
+    for (uint32_t bad = s_bad[tid >> 6]; bad; bad &= bad - 1) {
+        const uint32_t row = place.row + 32 * (tid >> 6) + __builtin_ctz(bad);
+        row_plain<D, kE4m3>(a, place.request, sp, row / a.group, head * a.group + row % a.group, flags);
+    }
 }
 
 // A request's rows decide which kernel computes it; the host knows only the
@@ -651,6 +858,17 @@ bool has_few(const AttentionLaunch& a) {
     return a.max_new * uint64_t(a.group) <= kSplitRows || uint64_t(a.max_new) * a.requests > a.tokens;
 }
 
+bool has_many(const AttentionLaunch& a) { return a.max_new * uint64_t(a.group) > kSplitRows; }
+
+// Runs that the keys of a tile are cut into: enough for two workgroups a CU,
+// each run at least 8 tiles of keys long where every request is as long as
+// its table allows.
+uint32_t splits_of(const AttentionLaunch& a) {
+    const uint64_t groups = uint64_t(tile_count(a)) * a.heads;
+    const uint64_t most = ((uint64_t(a.width) << a.page_shift) + 8 * kTileKeys - 1) / (8 * kTileKeys);
+    return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({512 / groups, most, 32})));
+}
+
 template <int D, bool kE4m3>
 hipError_t launch(AttentionLaunch a, void* work, hipStream_t stream) {
     a.least_rows = has_few(a) ? kSplitRows : 0;
@@ -658,17 +876,23 @@ hipError_t launch(AttentionLaunch a, void* work, hipStream_t stream) {
         attention_split<D, kE4m3><<<kParts, Split<D, kE4m3>::kWaves * 64, 0, stream>>>(a, work);
         attention_combine<D, kE4m3><<<dim3(a.heads, a.requests), 256, 0, stream>>>(a, work);
     }
-    if (a.max_new * uint64_t(a.group) > kSplitRows) {
-        const dim3 grid((a.max_new + 3) / 4, a.heads * a.group, a.requests);
-        attention_rows<D, kE4m3><<<grid, 256, 0, stream>>>(a);
+    if (has_many(a)) {
+        const uint32_t splits = splits_of(a), groups = tile_count(a) * a.heads;
+        attention_tiles<D, kE4m3><<<dim3(groups, splits), 256, 0, stream>>>(a, work);
+        if (splits > 1) attention_tile_combine<D, kE4m3><<<groups, 256, 0, stream>>>(a, work, splits);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
+// The two kernels' parts may share the memory: the stream runs one after the other.
 uint64_t attention_work_bytes(const AttentionLaunch& a, uint32_t head_dim) {
-    return has_few(a) ? uint64_t(kParts) * 2 * kSplitRows * (head_dim + 2) * 4 : 256;
+    uint64_t need = 256;
+    if (has_few(a)) need = std::max<uint64_t>(need, uint64_t(kParts) * 2 * kSplitRows * (head_dim + 2) * 4);
+    if (has_many(a) && splits_of(a) > 1)
+        need = std::max<uint64_t>(need, uint64_t(tile_count(a)) * a.heads * splits_of(a) * kTileRows * (head_dim + 2) * 4);
+    return need;
 }
 
 hipError_t launch_attention(const AttentionLaunch& a, uint32_t head_dim, uint32_t dtype, void* work,

@@ -156,47 +156,64 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
     return u.v;
 }
 
-// The two k-steps 2p, 2p + 1 of K's A operand for 32 keys from row0: dims 32p
-// .. 32p + 31.  bf16: two 16-byte reads, lane half h holds dims 16s + 8h..;
-// e4m3: one 16-byte read, dims 32p + 16h .. + 15, the first 8 for step 2p (Q
-// is loaded to match, see load_q).
+// LDS addresses of a lane's operands.  A swizzled chunk index is an exclusive
+// or, and the row offsets used (multiples of 16 and 32) do not change the
+// swizzle, so one base per lane and exclusive ors with constants give every
+// address, with tile, row and stage as constant offsets.
+//
+// K's A operand for k-steps 2p, 2p + 1 of 32 keys.  bf16: two 16-byte reads,
+// the lane's half h holds dims 16s + 8h..; e4m3: one 16-byte read, dims 32p +
+// 16h .. + 15, the first 8 for step 2p (Q is loaded to match, see load_q).
 template <int D, bool kE4m3>
-__device__ __forceinline__ void read_k(const uint8_t* tile, uint32_t row0, int p, uint32_t lane, bf16x8 (&k)[2]) {
+__device__ __forceinline__ uint32_t base_k(uint32_t lane) {
     using T = Tile<D, kE4m3>;
-    const uint32_t r = row0 + (lane & 31), h = lane >> 5, sw = T::swizzle_k(r);
+    const uint32_t r = lane & 31, h = lane >> 5;
+    return r * T::kRow + ((h ^ T::swizzle_k(r)) << 4);
+}
+
+template <int D, bool kE4m3>
+__device__ __forceinline__ void read_k(uint32_t base, uint32_t offset, int p, bf16x8 (&k)[2]) {
     if constexpr (!kE4m3) {
         for (int i = 0; i < 2; ++i)
-            k[i] = *reinterpret_cast<const bf16x8*>(tile + r * T::kRow + (((4 * p + 2 * i + h) ^ sw) << 4));
+            k[i] = *reinterpret_cast<SKV_LDS(const bf16x8)>((base ^ uint32_t(64 * p + 32 * i)) + offset);
     } else {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(tile + r * T::kRow + (((2 * p + h) ^ sw) << 4));
+        const u32x4 x = *reinterpret_cast<SKV_LDS(const u32x4)>((base ^ uint32_t(32 * p)) + offset);
         k[0] = widen(x[0], x[1]);
         k[1] = widen(x[2], x[3]);
     }
 }
 
 // V^T's A operand: dims 32 dt + lane % 32, the 8 keys of the lane's half of
-// the 16 keys from row0 (see above for their order).
+// 16 keys (see above for their order).  The transposing reads give 16 lanes
+// the columns of a matrix of 4 rows x 16 (16-bit) or 8 x 16 (8-bit) whose
+// rows 4 or 2 neighbouring lanes address.
 template <int D, bool kE4m3>
-__device__ __forceinline__ bf16x8 read_v(const uint8_t* tile, uint32_t row0, int dt, uint32_t lane) {
+__device__ __forceinline__ uint32_t base_v(uint32_t lane) {
     using T = Tile<D, kE4m3>;
     const uint32_t h = lane >> 5, side = (lane >> 4) & 1, i = lane & 15;
+    if constexpr (!kE4m3) {
+        const uint32_t r = 4 * h + (i >> 2);
+        return r * T::kRow + (((2 * side + ((i & 3) >> 1)) ^ T::swizzle_v(r)) << 4) + 8 * (i & 1);
+    } else {
+        const uint32_t j = i >> 1, r = 4 * h + (j & 3) + 2 * (j & 4);
+        return r * T::kRow + ((side ^ T::swizzle_v(r)) << 4) + 8 * (i & 1);
+    }
+}
+
+template <int D, bool kE4m3>
+__device__ __forceinline__ bf16x8 read_v(uint32_t base, uint32_t offset, int dt) {
     if constexpr (!kE4m3) {
         union {
             s16x4 q[2];
             bf16x8 v;
         } u;
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t r = row0 + 8 * e + 4 * h + (i >> 2);
-            const uint32_t byte = 64 * dt + 32 * side + 8 * (i & 3);
-            const uint8_t* at = tile + r * T::kRow + ((((byte >> 4) ^ T::swizzle_v(r)) << 4) | (byte & 8));
-            u.q[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SKV_LDS(s16x4))at);
-        }
+        for (int e = 0; e < 2; ++e)
+            u.q[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<SKV_LDS(s16x4)>(
+                (base ^ uint32_t(64 * dt)) + offset + 8 * e * Tile<D, kE4m3>::kRow));
         return u.v;
     } else {
-        const uint32_t j = i >> 1, r = row0 + 4 * h + (j & 3) + 2 * (j & 4);
-        const uint32_t c = 2 * dt + side;
-        const uint8_t* at = tile + r * T::kRow + (((c ^ T::swizzle_v(r)) << 4) | 8 * (i & 1));
-        const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((SKV_LDS(i32x2))at);
+        const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            reinterpret_cast<SKV_LDS(i32x2)>((base ^ uint32_t(32 * dt)) + offset));
         return widen(uint32_t(x[0]), uint32_t(x[1]));
     }
 }
@@ -243,26 +260,30 @@ struct Rows {
     }
 };
 
-// One tile of 32 * NM keys: scores, masked where key > `limit` (relative to
-// the tile; the lane's own row), the running maximum, probabilities, and
-// their product with V.  factor > 0: scale in base-2 units.
-template <int D, bool kE4m3, int NM, bool kMask>
-__device__ __forceinline__ void tile_step(const uint8_t* kt, const uint8_t* vt, const bf16x8 (&q)[D / 16], float factor,
+// One tile of 32 * NM keys (kt, vt: the lane's LDS bases in it): scores,
+// masked (where `mask`, the same for the wave) past key `limit` of the tile,
+// the running maximum, probabilities, and their product with V.  factor > 0:
+// scale in base-2 units.
+template <int D, bool kE4m3, int NM>
+__device__ __forceinline__ void tile_step(uint32_t kt, uint32_t vt, const bf16x8 (&q)[D / 16], float factor, bool mask,
                                           int limit, uint32_t lane, Rows<D>& st) {
+    constexpr int kRow = Tile<D, kE4m3>::kRow;
     f32x16 s[NM];
 #pragma unroll
-    for (int t = 0; t < NM; ++t) {
+    for (int t = 0; t < NM; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
 #pragma unroll
-        for (int p = 0; p < D / 32; ++p) {
+    for (int p = 0; p < D / 32; ++p) {
+#pragma unroll
+        for (int t = 0; t < NM; ++t) {
             bf16x8 k[2];
-            read_k<D, kE4m3>(kt, 32 * t, p, lane, k);
+            read_k<D, kE4m3>(kt, 32 * t * kRow, p, k);
             s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[0], q[2 * p], s[t], 0, 0, 0);
             s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[1], q[2 * p + 1], s[t], 0, 0, 0);
         }
     }
-    if (kMask) {
+    if (mask) {
         const int lim = limit - 4 * int(lane >> 5);
 #pragma unroll
         for (int t = 0; t < NM; ++t)
@@ -306,7 +327,7 @@ __device__ __forceinline__ void tile_step(const uint8_t* kt, const uint8_t* vt, 
             }
 #pragma unroll
             for (int dt = 0; dt < D / 32; ++dt)
-                st.o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v<D, kE4m3>(vt, 32 * t + 16 * hf, dt, lane), p.v,
+                st.o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read_v<D, kE4m3>(vt, (32 * t + 16 * hf) * kRow, dt), p.v,
                                                                    st.o[dt], 0, 0, 0);
         }
     }
@@ -484,6 +505,7 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
         uint32_t t0 = c0 * step + wave * G::kKeys;                       // the tile in use
         const uint32_t stop = min(c1 * step, sp.len);
         const uint32_t lds0 = lds_address(&s_tiles[wave][0][0]);
+        const uint32_t lane_k = lds0 + base_k<D, kE4m3>(lane), lane_v = lds0 + G::kStage / 2 + base_v<D, kE4m3>(lane);
         // lane j looks up token j of a tile (and j + 64 where tiles are that long)
         constexpr int kLook = G::kKeys > 64 ? 2 : 1;
         auto look_up = [&](uint32_t at, int32_t (&e)[kLook]) {
@@ -520,11 +542,9 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
                     look_up(t0 + 2 * step, next);
                     load_tile(t0 + step, e, stage ^ 1);
                 }
-                const uint8_t* kt = &s_tiles[wave][stage][0];
-                if (int(t0) + G::kKeys - 1 > first_limit)
-                    tile_step<D, kE4m3, G::kKeys / 32, true>(kt, kt + G::kStage / 2, q, factor, limit - int(t0), lane, st);
-                else
-                    tile_step<D, kE4m3, G::kKeys / 32, false>(kt, kt + G::kStage / 2, q, factor, 0, lane, st);
+                const uint32_t kt = lane_k + stage * G::kStage, vt = lane_v + stage * G::kStage;
+                tile_step<D, kE4m3, G::kKeys / 32>(kt, vt, q, factor, int(t0) + G::kKeys - 1 > first_limit,
+                                                   limit - int(t0), lane, st);
             }
         }
         // join the waves: sums to LDS (each into its own tiles), then every thread takes some of a row's values
@@ -695,7 +715,7 @@ __device__ __forceinline__ float* tile_slot(void* work, uint64_t id) {
 template <int D, bool kE4m3>
 struct TileGeo {
     static constexpr int kStage = 2 * kTileKeys * Tile<D, kE4m3>::kRow;
-    static constexpr int kPerCu = 2 * kStage > 80 * 1024 ? 1 : 2;        // workgroups that fit a CU's LDS
+    static constexpr int kPerCu = D == 256 ? 1 : 2;        // workgroups a CU holds: registers, and 160 KB of LDS
 };
 
 template <int D, bool kE4m3>
@@ -737,7 +757,8 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
 
     const uint8_t* kb = a.k_pages + int64_t(head) * a.head_stride;
     const uint8_t* vb = a.v_pages + int64_t(head) * a.head_stride;
-    const uint32_t lds0 = lds_address(&s_tiles[0][0]) + wave * kWaveRows * T::kRow;
+    const uint32_t lds = lds_address(&s_tiles[0][0]), lds0 = lds + wave * kWaveRows * T::kRow;
+    const uint32_t lane_k = lds + base_k<D, kE4m3>(lane), lane_v = lds + G::kStage / 2 + base_v<D, kE4m3>(lane);
     // a wave brings in 16 of the 64 keys; lane j looks up the j-th of them
     auto token_of = [&](uint32_t at) { return min(at + wave * kWaveRows + (lane & 15), sp.len - 1); };
     auto look_up = [&](uint32_t at) { return a.table[int64_t(b) * a.table_stride + (token_of(at) >> a.page_shift)]; };
@@ -758,8 +779,8 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
     if (begin < end) {
         int32_t entry = look_up(begin), next = look_up(begin + kTileKeys);
         load_tile(begin, entry, 0);
-        uint32_t stage = 0;
-        for (uint32_t t0 = begin; t0 < end; t0 += kTileKeys, stage ^= 1) {
+        uint32_t stage = 0, t0 = begin;
+        auto advance = [&] {               // tile t0 is there; the one after it is on its way
             wait_loads();
             __syncthreads();
             if (t0 + kTileKeys < end) {
@@ -767,13 +788,14 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
                 next = look_up(t0 + 2 * kTileKeys);
                 load_tile(t0 + kTileKeys, entry, stage ^ 1);
             }
-            const uint8_t* kt = &s_tiles[stage][0];
-            if (int(t0) >= any_sees) continue;
-            if (int(t0 + kTileKeys) > all_see)
-                tile_step<D, kE4m3, kTileKeys / 32, true>(kt, kt + G::kStage / 2, q, factor, limit - int(t0), lane, st);
-            else
-                tile_step<D, kE4m3, kTileKeys / 32, false>(kt, kt + G::kStage / 2, q, factor, 0, lane, st);
+        };
+        // the wave's own rows may be done before the workgroup's last ones
+        for (const uint32_t own = min(end, uint32_t(any_sees)); t0 < own; t0 += kTileKeys, stage ^= 1) {
+            advance();
+            tile_step<D, kE4m3, kTileKeys / 32>(lane_k + stage * G::kStage, lane_v + stage * G::kStage, q, factor,
+                                                int(t0 + kTileKeys) > all_see, limit - int(t0), lane, st);
         }
+        for (; t0 < end; t0 += kTileKeys, stage ^= 1) advance();
     }
     const float l = half_sum(st.l);
     if (gridDim.y > 1) {

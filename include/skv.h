@@ -410,8 +410,8 @@ int skv_store_stats(skv_store* store, skv_store_info* stats);
  *
  * K and V of one layer are two arrays of the same strides,
  *   [pages][page_tokens][heads][head_dim], head_dim contiguous,
- * any of the other strides (in elements; each a multiple of 16 bytes, the
- * base 16-byte aligned, else SKV_ERR_ARG), so head-major pools, slices of a
+ * any of the other strides (in elements; each a multiple of 16 bytes unless
+ * its dimension has one element, the base 16-byte aligned, else SKV_ERR_ARG), so head-major pools, slices of a
  * whole-cache array [layers][K|V][...] and the codec's own contiguous arrays
  * (pages of 128 consecutive tokens) all qualify.  dtype: SKV_BF16, or
  * SKV_E4M3 with a scale per head, value = code * scale[head] (NULL: 1).

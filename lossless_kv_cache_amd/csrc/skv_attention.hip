@@ -138,7 +138,9 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // wait for every such load; no register is written, so nothing can be reused
 // too early.
 __device__ __forceinline__ void load_lds16(const uint8_t* g, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                 "v"(g)
+                 : "memory");
 }
 // Every load above has landed and every LDS read before has its data.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
@@ -337,20 +339,25 @@ __device__ __forceinline__ void tile_step(uint32_t kt, uint32_t vt, const bf16x8
 // The keys of every (request, KV head) are cut into units of kWaves * kKeys
 // tokens, all units numbered through, and each of kParts workgroups takes an
 // equal run of them: the cache is read once and evenly however different the
-// lengths are.  A workgroup's run covers whole (request, head)s, which it
-// finishes, and at most two broken ones (its first and last), whose
-// unnormalized sums go to the workspace for attention_combine.
+// lengths are.  A (request, head) counts one unit more than it has keys for,
+// about what joining its waves costs.  A workgroup's run covers whole
+// (request, head)s, which it finishes, and at most two broken ones (its first
+// and last), whose unnormalized sums go to the workspace for
+// attention_combine.
 //
-// A wave keeps two tiles of 16 KB in LDS of its own: one being used, the
-// other on its way straight from memory, 64 KB in flight per CU.
+// A wave keeps two tiles of 16 KB (32 KB for D = 256) in LDS of its own: one
+// being used, the other on its way straight from memory, 64 KB in flight per
+// CU.  The next (request, head)'s first tile is on its way while the waves
+// of the last one are joined.
 constexpr uint32_t kSplitRows = 32;
 
 template <int D, bool kE4m3>
 struct Split {
-    static constexpr int kWaves = D == 256 && !kE4m3 ? 2 : 4;
-    static constexpr int kStage = kWaves == 2 ? 32768 : 16384;             // bytes of K and V per wave
+    static constexpr int kWaves = D == 256 ? 2 : 4;
+    static constexpr int kStage = D == 256 ? 32768 : 16384;                // bytes of K and V per wave
     static constexpr int kKeys = kStage / 2 / Tile<D, kE4m3>::kRow;         // per wave and tile
     static constexpr int kUnit = kWaves * kKeys;
+    static_assert(kSplitRows * D * 4 <= kStage, "the join's sums of a wave fit one tile");
 };
 
 constexpr uint32_t kParts = 256;      // one workgroup per CU (128 KB of LDS)
@@ -361,12 +368,12 @@ struct Units {
     uint32_t request;
 };
 
-// Units of one head of request b: at least one where it has queries at all,
-// so that rows that see no key get their zeros.
+// Units of one head of request b: one even where it has no keys, so that rows
+// that see none get their zeros.
 __device__ __forceinline__ uint32_t units_of(const AttentionLaunch& a, uint32_t b, uint32_t unit, uint32_t& flags) {
     const Span s = span_of(a, b, flags);
     if (s.n == 0 || s.n * a.group > kSplitRows) return 0;
-    return max(1u, (s.len + unit - 1) / unit);
+    return 1 + (s.len + unit - 1) / unit;
 }
 
 // Sum over the workgroup's threads of x (kThreads of them), to all.
@@ -389,34 +396,48 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* s_wave, uin
     return x;                          // inclusive
 }
 
+// A value that is the same in every lane, where the compiler can see that it is.
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return uint64_t(__builtin_amdgcn_readfirstlane(uint32_t(x >> 32))) << 32 |
+           uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(x)));
+}
+
 // The batch's units and, with find(total) naming a unit, the request it
 // belongs to and that request's first unit.  s_out: LDS for the answer.
 template <int kThreads, class Find>
 __device__ Units find_units(const AttentionLaunch& a, uint32_t unit, uint32_t& flags, Find find, uint64_t* s_wave,
                             uint64_t* s_out) {
     Units u{0, 0, a.requests};
-    uint64_t mine = 0, total;
-    for (uint32_t b = threadIdx.x; b < a.requests; b += kThreads) mine += units_of(a, b, unit, flags);
-    (void)block_scan<kThreads>(mine, s_wave, &total);
-    u.total = total * a.heads;
-    const uint64_t at = find(u.total);
-    if (at >= u.total) return u;
-    uint64_t before = 0;
+    uint64_t total, at = 0, before = 0;
+    const bool once = a.requests <= kThreads;           // one sum gives the total and every request's place
+    if (!once) {
+        uint64_t mine = 0;
+        for (uint32_t b = threadIdx.x; b < a.requests; b += kThreads) mine += units_of(a, b, unit, flags);
+        (void)block_scan<kThreads>(mine, s_wave, &total);
+        u.total = total * a.heads;
+        at = find(u.total);
+    }
     uint32_t ignore = 0;
     for (uint32_t base = 0; base < a.requests; base += kThreads) {
         const uint32_t b = base + threadIdx.x;
-        const uint64_t n = b < a.requests ? units_of(a, b, unit, ignore) : 0;
+        const uint64_t n = b < a.requests ? units_of(a, b, unit, once ? flags : ignore) : 0;
         const uint64_t end = before + block_scan<kThreads>(n, s_wave, &total);
+        before += total;
+        if (once) {
+            u.total = total * a.heads;
+            at = find(u.total);
+        }
         if (n && at >= (end - n) * a.heads && at < end * a.heads) {
             s_out[0] = (end - n) * a.heads;
             s_out[1] = b;
         }
-        before += total;
         if (at < before * a.heads) break;
     }
     __syncthreads();
-    u.first = s_out[0];
-    u.request = uint32_t(s_out[1]);
+    u.total = uniform(u.total);
+    if (uniform(at) >= u.total) return u;
+    u.first = uniform(s_out[0]);
+    u.request = uint32_t(uniform(s_out[1]));
     return u;
 }
 
@@ -456,101 +477,115 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
     using G = Split<D, kE4m3>;
     using T = Tile<D, kE4m3>;
     constexpr int kThreads = G::kWaves * 64, kLoads = G::kStage / 2 / 1024, kLanes = 64 / T::kRowsPerLoad;
+    constexpr int kLook = G::kKeys > 64 ? 2 : 1;         // lane j looks up token j of a tile (and j + 64)
     __shared__ __align__(1024) uint8_t s_tiles[G::kWaves][2][G::kStage];
     __shared__ float s_m[G::kWaves][kSplitRows], s_l[G::kWaves][kSplitRows];
     __shared__ uint64_t s_wave[G::kWaves], s_found[2];
-    __shared__ uint32_t s_bad;
+    __shared__ uint32_t s_bad, s_stage[G::kWaves];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t part = blockIdx.x;
-    uint32_t flags = 0;
-    Units un = find_units<kThreads>(a, G::kUnit, flags, [&](uint64_t total) { return part_begin(total, part); }, s_wave,
-                                    s_found);
+    const uint32_t part = blockIdx.x, row = lane & 31;
+    uint32_t flags = 0, ignore = 0;
+    const Units un = find_units<kThreads>(a, G::kUnit, flags, [&](uint64_t total) { return part_begin(total, part); },
+                                          s_wave, s_found);
     if (part == 0 && flags && a.status) atomicOr(a.status, flags);
-    uint64_t u = part_begin(un.total, part);
-    const uint64_t begin = u, end = part_begin(un.total, part + 1);
-    if (u >= end) return;
     flags = 0;
-    uint32_t b = un.request, ignore = 0;
-    uint64_t first = un.first;
-    uint32_t units = units_of(a, b, G::kUnit, ignore);
-    Span sp = span_of(a, b, ignore);
+    const uint64_t begin = part_begin(un.total, part), end = part_begin(un.total, part + 1);
+    if (begin >= end) return;
+    const uint32_t lds0 = lds_address(&s_tiles[wave][0][0]);
+    const uint32_t lane_k = lds0 + base_k<D, kE4m3>(lane), lane_v = lds0 + G::kStage / 2 + base_v<D, kE4m3>(lane);
 
-    while (u < end) {
-        // the request and head of unit u, and the run of its units that is ours
-        while (u - first >= uint64_t(units) * a.heads || units == 0) {
+    // the request and head of unit u, the run of its units that is ours, and what its rows need
+    uint64_t u = begin, first = un.first;
+    uint32_t b = un.request, units = units_of(a, b, G::kUnit, ignore);
+    Span sp = span_of(a, b, ignore);
+    uint32_t head, run, t0, stop;
+    bool whole;
+    float raw;
+    int first_limit, limit;
+    bf16x8 q[D / 16];
+    int32_t next[kLook];
+    uint32_t stage = 1;
+    const uint8_t *kb, *vb;
+    auto look_up = [&](uint32_t at, int32_t (&e)[kLook]) __attribute__((always_inline)) {
+        for (int i = 0; i < kLook; ++i)
+            e[i] = a.table[int64_t(b) * a.table_stride + (min(at + 64 * i + lane, sp.len - 1) >> a.page_shift)];
+    };
+    auto load_tile = [&](uint32_t at, const int32_t (&e)[kLook], uint32_t to) __attribute__((always_inline)) {
+        int64_t off[kLook];
+        for (int i = 0; i < kLook; ++i) {
+            const uint32_t token = min(at + 64 * i + lane, sp.len - 1);
+            bool bad = false;
+            const uint32_t page = page_or_zero(e[i], a.pages, &bad);
+            if (bad) flags |= SKV_PAGES_PAGE;
+            off[i] = int64_t(page) * a.page_stride + int64_t(token & ((1u << a.page_shift) - 1)) * a.token_stride;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t r = i * T::kRowsPerLoad + lane / kLanes, c = lane % kLanes;
+            const int64_t o = __shfl(off[(i * T::kRowsPerLoad) / 64], int(r & 63));
+            load_lds16(kb + o + ((c ^ T::swizzle_k(r)) << 4), lds0 + to * G::kStage + i * 1024);
+            load_lds16(vb + o + ((c ^ T::swizzle_v(r)) << 4), lds0 + to * G::kStage + G::kStage / 2 + i * 1024);
+        }
+    };
+    // Unit u's (request, head): its rows' queries and its first tile, into the stage that is not in use.
+    auto open = [&]() __attribute__((always_inline)) -> bool {
+        while (units == 0 || u - first >= uint64_t(units) * a.heads) {
             first += uint64_t(units) * a.heads;
-            if (++b >= a.requests) return;
+            if (++b >= a.requests) return false;
             units = units_of(a, b, G::kUnit, ignore);
             sp = span_of(a, b, ignore);
         }
-        const uint32_t head = uint32_t((u - first) / units), c0 = uint32_t((u - first) % units);
-        const uint32_t c1 = uint32_t(min(uint64_t(units), c0 + (end - u)));
-        const bool whole = c0 == 0 && c1 == units;
-        const uint32_t rows = sp.n * a.group, row = lane & 31;
+        head = uint32_t((u - first) / units);
+        const uint32_t c0 = uint32_t((u - first) % units), c1 = uint32_t(min(uint64_t(units), c0 + (end - u)));
+        run = c1 - c0;
+        whole = run == units;
         const uint32_t qi = row / a.group, qg = row - qi * a.group;
-        const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
-        const float raw = a.scale * (a.k_scale ? a.k_scale[head] : 1.0f);
-        const float factor = raw == 0.0f ? 1.0f : fabsf(raw) * kLog2e;
-        bf16x8 q[D / 16];
-        load_q<D, kE4m3>(a.q + int64_t(sp.row + qi) * a.q_token + int64_t(head * a.group + qg) * a.q_head, row < rows,
-                         raw, lane, q);
-        const int first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;     // of query 0
-        const int limit = row < rows ? first_limit + (a.causal ? int(qi) : 0) : -1;
-        Rows<D> st;
-        st.clear();
-
-        const uint8_t* kb = a.k_pages + int64_t(head) * a.head_stride;
-        const uint8_t* vb = a.v_pages + int64_t(head) * a.head_stride;
-        const uint32_t step = G::kUnit;
-        uint32_t t0 = c0 * step + wave * G::kKeys;                       // the tile in use
-        const uint32_t stop = min(c1 * step, sp.len);
-        const uint32_t lds0 = lds_address(&s_tiles[wave][0][0]);
-        const uint32_t lane_k = lds0 + base_k<D, kE4m3>(lane), lane_v = lds0 + G::kStage / 2 + base_v<D, kE4m3>(lane);
-        // lane j looks up token j of a tile (and j + 64 where tiles are that long)
-        constexpr int kLook = G::kKeys > 64 ? 2 : 1;
-        auto look_up = [&](uint32_t at, int32_t (&e)[kLook]) {
-            for (int i = 0; i < kLook; ++i)
-                e[i] = a.table[int64_t(b) * a.table_stride + (min(at + 64 * i + lane, sp.len - 1) >> a.page_shift)];
-        };
-        auto load_tile = [&](uint32_t at, const int32_t (&e)[kLook], uint32_t stage) {
-            int64_t off[kLook];
-            for (int i = 0; i < kLook; ++i) {
-                const uint32_t token = min(at + 64 * i + lane, sp.len - 1);
-                bool bad = false;
-                const uint32_t page = page_or_zero(e[i], a.pages, &bad);
-                if (bad) flags |= SKV_PAGES_PAGE;
-                off[i] = int64_t(page) * a.page_stride + int64_t(token & ((1u << a.page_shift) - 1)) * a.token_stride;
-            }
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const uint32_t r = i * T::kRowsPerLoad + lane / kLanes, c = lane % kLanes;
-                const int64_t o = __shfl(off[(i * T::kRowsPerLoad) / 64], int(r & 63));
-                load_lds16(kb + o + ((c ^ T::swizzle_k(r)) << 4), lds0 + stage * G::kStage + i * 1024);
-                load_lds16(vb + o + ((c ^ T::swizzle_v(r)) << 4), lds0 + stage * G::kStage + G::kStage / 2 + i * 1024);
-            }
-        };
+        const bool have = row < sp.n * a.group;
+        raw = a.scale * (a.k_scale ? a.k_scale[head] : 1.0f);
+        first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;          // of query 0
+        limit = have ? first_limit + (a.causal ? int(qi) : 0) : -1;
+        kb = a.k_pages + int64_t(head) * a.head_stride;
+        vb = a.v_pages + int64_t(head) * a.head_stride;
+        t0 = c0 * G::kUnit + wave * G::kKeys;
+        stop = min(c1 * G::kUnit, sp.len);
         if (t0 < stop) {
             int32_t e[kLook];
             look_up(t0, e);
-            int32_t next[kLook];
-            look_up(t0 + step, next);
-            load_tile(t0, e, 0);
-            for (uint32_t stage = 0; t0 < stop; t0 += step, stage ^= 1) {
-                wait_loads();
-                if (t0 + step < stop) {
-                    for (int i = 0; i < kLook; ++i) e[i] = next[i];
-                    look_up(t0 + 2 * step, next);
-                    load_tile(t0 + step, e, stage ^ 1);
-                }
-                const uint32_t kt = lane_k + stage * G::kStage, vt = lane_v + stage * G::kStage;
-                tile_step<D, kE4m3, G::kKeys / 32>(kt, vt, q, factor, int(t0) + G::kKeys - 1 > first_limit,
-                                                   limit - int(t0), lane, st);
-            }
+            look_up(t0 + G::kUnit, next);
+            load_q<D, kE4m3>(a.q + int64_t(sp.row + qi) * a.q_token + int64_t(head * a.group + qg) * a.q_head, have, raw,
+                             lane, q);
+            load_tile(t0, e, stage ^ 1);
         }
-        // join the waves: sums to LDS (each into its own tiles), then every thread takes some of a row's values
-        wait_loads();
+        return true;
+    };
+
+    bool more = open();
+    while (more) {
+        const float factor = raw == 0.0f ? 1.0f : fabsf(raw) * kLog2e;
+        Rows<D> st;
+        st.clear();
+        for (; t0 < stop; t0 += G::kUnit) {
+            stage ^= 1;
+            wait_loads();
+            if (t0 + G::kUnit < stop) {
+                int32_t e[kLook];
+                for (int i = 0; i < kLook; ++i) e[i] = next[i];
+                look_up(t0 + 2 * G::kUnit, next);
+                load_tile(t0 + G::kUnit, e, stage ^ 1);
+            }
+            tile_step<D, kE4m3, G::kKeys / 32>(lane_k + stage * G::kStage, lane_v + stage * G::kStage, q, factor,
+                                               int(t0) + G::kKeys - 1 > first_limit, limit - int(t0), lane, st);
+        }
+        // what is joined now, before the next one's state takes its place
+        const Span was = sp;
+        const uint32_t was_b = b, was_head = head, rows = sp.n * a.group, slot_at = u != begin;
+        const bool was_whole = whole;
+        const int was_limit = first_limit;
+        u += run;
+        more = u < end && open();
+        // the sums of each wave to LDS, into the stage it used last; then every thread takes some of a row's values
         if (row < rows) {
-            f32x4* mine = reinterpret_cast<f32x4*>(&s_tiles[wave][0][0]) + row * (D / 4);
+            f32x4* mine = reinterpret_cast<f32x4*>(&s_tiles[wave][stage][0]) + row * (D / 4);
 #pragma unroll
             for (int t = 0; t < D / 32; ++t)
 #pragma unroll
@@ -563,9 +598,11 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
                 s_l[wave][row] = l;
             }
         }
+        if (lane == 0) s_stage[wave] = stage;
         if (tid == 0) s_bad = 0;
         __syncthreads();
-        float* slot = part_slot<D>(work, part, u != begin);
+        const float vs = a.v_scale ? a.v_scale[was_head] : 1.0f;
+        float* slot = part_slot<D>(work, part, slot_at);
         for (uint32_t i = tid; i < rows * (D / 4); i += kThreads) {
             const uint32_t r = i / (D / 4), f = i % (D / 4);
             float top = s_m[0][r], l = 0.0f;
@@ -574,15 +611,15 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
             for (int w = 0; w < G::kWaves; ++w) {
                 const float k = exp2_diff(s_m[w][r], top);
                 l += k * s_l[w][r];
-                o += k * reinterpret_cast<const f32x4*>(&s_tiles[w][0][0])[r * (D / 4) + (f ^ (r & 7))];
+                if (s_m[w][r] != -INFINITY)        // else all its keys were hidden, and o may be 0 * NaN
+                    o += k * reinterpret_cast<const f32x4*>(&s_tiles[w][s_stage[w]][0])[r * (D / 4) + (f ^ (r & 7))];
             }
-            if (whole) {
-                const uint32_t ri = r / a.group, qh = head * a.group + r - ri * a.group;
-                const bool none = first_limit + (a.causal ? int(ri) : 0) < 0;
-                const float inv = vs / l;
-                const bool nan = store_out(a, sp.row + ri, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : o * inv);
-                if (nan && a.causal && sp.n > 1) atomicOr(&s_bad, 1u << r);
-                if (f == 0) store_lse(a, sp.row + ri, qh, none ? -INFINITY : top, none ? 1.0f : l);
+            if (was_whole) {
+                const uint32_t ri = r / a.group, qh = was_head * a.group + r - ri * a.group;
+                const bool none = was_limit + (a.causal ? int(ri) : 0) < 0;
+                const bool nan = store_out(a, was.row + ri, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : o * (vs / l));
+                if (nan && a.causal && was.n > 1) atomicOr(&s_bad, 1u << r);
+                if (f == 0) store_lse(a, was.row + ri, qh, none ? -INFINITY : top, none ? 1.0f : l);
             } else {
                 *reinterpret_cast<f32x4*>(slot + r * D + 4 * f) = o;
                 if (f == 0) {
@@ -594,62 +631,108 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
         __syncthreads();
         // A NaN in a value that only later queries see has reached a row through 0 * NaN in a shared tile: such
         // rows (and those whose NaN is their own) are computed again, key after key.
-        for (uint32_t r = 0, bad = s_bad; r < rows; ++r)
-            if ((bad >> r & 1) && r % G::kWaves == wave)
-                row_plain<D, kE4m3>(a, b, sp, r / a.group, head * a.group + r % a.group, flags);
-        __syncthreads();
-        u += c1 - c0;
+        if (was_whole && a.causal && was.n > 1) {
+            for (uint32_t r = 0, bad = s_bad; r < rows; ++r)
+                if ((bad >> r & 1) && r % G::kWaves == wave)
+                    row_plain<D, kE4m3>(a, was_b, was, r / a.group, was_head * a.group + r % a.group, flags);
+            __syncthreads();
+        }
     }
     if (flags && a.status) atomicOr(a.status, flags);
+}
+
+// Partial sums (m in base-2 units, l, o) read kAtOnce at a time: their loads are in flight together.
+struct Joined {
+    float m, l;
+    f32x4 o;
+};
+
+template <int D, class Slot>
+__device__ __forceinline__ Joined join_parts(uint32_t from, uint32_t to, uint32_t rows, uint32_t r, uint32_t f, Slot slot_of) {
+    constexpr uint32_t kAtOnce = 8;
+    Joined j{-INFINITY, 0.0f, f32x4{0, 0, 0, 0}};
+    for (uint32_t p = from; p < to; p += kAtOnce) {
+        float m[kAtOnce], l[kAtOnce];
+        f32x4 o[kAtOnce];
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) {
+            const float* slot = slot_of(min(p + i, to - 1));
+            m[i] = slot[rows * D + r];
+            l[i] = slot[rows * (D + 1) + r];
+            o[i] = *reinterpret_cast<const f32x4*>(slot + r * D + 4 * f);
+        }
+        float top = j.m;
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) {
+            if (p + i >= to) m[i] = -INFINITY;
+            top = fmaxf(top, m[i]);
+        }
+        const float keep = exp2_diff(j.m, top);
+        j.l *= keep;
+        j.o *= keep;
+        j.m = top;
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) {
+            const float k = exp2_diff(m[i], top);
+            j.l += k * l[i];
+            if (m[i] != -INFINITY) j.o += k * o[i];    // else all its keys were hidden, and o may be 0 * NaN
+        }
+    }
+    return j;
 }
 
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(256) attention_combine(AttentionLaunch a, const void* work) {
     using G = Split<D, kE4m3>;
-    __shared__ uint64_t s_wave[4];
+    __shared__ uint64_t s_sum[4][2];
     __shared__ uint32_t s_bad;
     const uint32_t head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     uint32_t flags = 0;
     const uint32_t units = units_of(a, b, G::kUnit, flags);
-    if (units == 0) return;
-    // this request's first unit: the sum of the earlier ones' units
-    uint64_t before = 0, rest = 0, total;
+    // the units of the earlier requests, and of all
+    uint64_t before = 0, all = 0;
     for (uint32_t i = tid; i < a.requests; i += 256) {
-        const uint32_t n = units_of(a, i, G::kUnit, flags);
+        const uint64_t n = units_of(a, i, G::kUnit, flags);
+        all += n;
         if (i < b) before += n;
-        else rest += n;
     }
-    (void)block_scan<256>(before, s_wave, &total);
-    before = total;
-    (void)block_scan<256>(rest, s_wave, &total);
-    const uint64_t all = (before + total) * a.heads, u0 = before * a.heads + uint64_t(head) * units, u1 = u0 + units;
+    for (uint32_t d = 32; d; d >>= 1) {
+        before += __shfl_xor(before, d);
+        all += __shfl_xor(all, d);
+    }
+    if ((tid & 63) == 0) {
+        s_sum[tid >> 6][0] = before;
+        s_sum[tid >> 6][1] = all;
+    }
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    if (units == 0) return;
+    before = all = 0;
+    for (int w = 0; w < 4; ++w) {
+        before += s_sum[w][0];
+        all += s_sum[w][1];
+    }
+    all *= a.heads;
+    const uint64_t u0 = before * a.heads + uint64_t(head) * units, u1 = u0 + units;
     // the part that has unit u: the last p with all * p / parts <= u
     const uint32_t p0 = uint32_t(((u0 + 1) * parts_of(all) - 1) / all), p1 = uint32_t((u1 * parts_of(all) - 1) / all);
     if (p0 == p1) return;              // finished by one workgroup
     const Span sp = span_of(a, b, flags);
-    const uint32_t rows = sp.n * a.group;
+    const uint32_t rows = sp.n * a.group, late = part_begin(all, p0) < u0;       // p0's slot: its first or its last
     const int first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;
     const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
     for (uint32_t i = tid; i < rows * (D / 4); i += 256) {
         const uint32_t r = i / (D / 4), f = i % (D / 4);
-        float top = -INFINITY, l = 0.0f;
-        f32x4 o{0, 0, 0, 0};
-        for (uint32_t p = p0; p <= p1; ++p) {
-            const float* slot = part_slot<D>(const_cast<void*>(work), p, part_begin(all, p) < u0);
-            const float m = slot[kSplitRows * D + r], next = fmaxf(top, m);
-            const float keep = exp2_diff(top, next), add = exp2_diff(m, next);
-            l = l * keep + slot[kSplitRows * (D + 1) + r] * add;
-            o = o * keep + *reinterpret_cast<const f32x4*>(slot + r * D + 4 * f) * add;
-            top = next;
-        }
+        const Joined j = join_parts<D>(p0, p1 + 1, kSplitRows, r, f, [&](uint32_t p) -> const float* {
+            return part_slot<D>(const_cast<void*>(work), p, p == p0 ? late : 0);
+        });
         const uint32_t ri = r / a.group, qh = head * a.group + r - ri * a.group;
         const bool none = first_limit + (a.causal ? int(ri) : 0) < 0;
-        const bool nan = store_out(a, sp.row + ri, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : o * (vs / l));
+        const bool nan = store_out(a, sp.row + ri, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : j.o * (vs / j.l));
         if (nan && a.causal && sp.n > 1) atomicOr(&s_bad, 1u << r);
-        if (f == 0) store_lse(a, sp.row + ri, qh, none ? -INFINITY : top, none ? 1.0f : l);
+        if (f == 0) store_lse(a, sp.row + ri, qh, none ? -INFINITY : j.m, none ? 1.0f : j.l);
     }
+    if (!a.causal || sp.n == 1) return;
     __syncthreads();
     for (uint32_t r = 0, bad = s_bad; r < rows; ++r)
         if ((bad >> r & 1) && r % 4 == (tid >> 6))
@@ -661,43 +744,16 @@ __global__ void __launch_bounds__(256) attention_combine(AttentionLaunch a, cons
 // the head's query heads, in that order, so all of them share the keys it
 // streams through LDS, 64 at a time, two tiles deep.  Each wave owns 32 rows.
 //
-// Tiles of query rows are numbered so that no sum over requests is needed:
-// request b's first is floor(starts[b] * group / 128) + b, which leaves it at
-// least ceil(n * group / 128) numbers.  The heads come fastest: eight
-// consecutive workgroups go to the eight XCDs, so with 8 KV heads (or a
-// divisor or multiple) each XCD's L2 holds the keys of its own heads.  The
-// last rows, which see the most keys, come first.
-//
-// With few tiles the keys are cut into `splits` runs whose unnormalized sums
-// attention_tile_combine joins.
+// Work is cut on the device, where the lengths are: a (tile of rows, head)
+// with more keys than kTileSlots-th of the whole work is cut into pieces of
+// that size, whose unnormalized sums attention_tile_combine joins; the
+// others are finished where they are computed.  Requests with the most keys
+// come first, and of a request the last rows, which see the most.  The heads
+// come fastest: eight consecutive workgroups go to the eight XCDs, so with 8
+// KV heads (or a divisor or multiple) each XCD's L2 holds the keys of its own
+// heads.
 constexpr uint32_t kTileRows = 128, kTileKeys = 64;
-
-struct TilePlace {
-    uint32_t request, row;             // request (none: a.requests), first of its rows
-    Span span;
-};
-
-__device__ __forceinline__ TilePlace find_tile(const AttentionLaunch& a, uint32_t tile, uint32_t& flags, uint32_t* s_at) {
-    if (threadIdx.x == 0) *s_at = a.requests;
-    __syncthreads();
-    for (uint32_t b = threadIdx.x; b < a.requests; b += blockDim.x) {
-        const Span s = span_of(a, b, flags);
-        const uint32_t rows = s.n * a.group, first = uint32_t(uint64_t(s.row) * a.group / kTileRows) + b;
-        if (rows > a.least_rows && tile >= first && tile - first < (rows + kTileRows - 1) / kTileRows) *s_at = b;
-    }
-    __syncthreads();
-    TilePlace t{*s_at, 0, Span{0, 0, 0}};
-    if (t.request < a.requests) {
-        uint32_t ignore = 0;
-        t.span = span_of(a, t.request, ignore);
-        t.row = (tile - (uint32_t(uint64_t(t.span.row) * a.group / kTileRows) + t.request)) * kTileRows;
-    }
-    return t;
-}
-
-__host__ __device__ __forceinline__ uint32_t tile_count(const AttentionLaunch& a) {
-    return uint32_t(uint64_t(a.tokens) * a.group / kTileRows) + a.requests;
-}
+constexpr uint32_t kLeastPiece = 4;        // tiles of keys: below, joining costs more than it spreads
 
 // Keys that rows up to `row` of a request see.
 __device__ __forceinline__ uint32_t keys_for(const AttentionLaunch& a, const Span& s, uint32_t row) {
@@ -705,6 +761,114 @@ __device__ __forceinline__ uint32_t keys_for(const AttentionLaunch& a, const Spa
     const uint32_t rows = s.n * a.group;
     const int64_t last = int64_t(s.len) - s.n + min(row, rows - 1) / a.group;
     return last < 0 ? 0 : uint32_t(last) + 1;
+}
+
+// Workgroups that run at the same time.
+__host__ __device__ constexpr uint32_t tile_slots(int head_dim) { return head_dim == 256 ? 256 : 512; }
+
+// Upper bound on the tiles of rows of one head, for the host.
+uint32_t tile_bound(const AttentionLaunch& a) {
+    return uint32_t(uint64_t(a.tokens) * a.group / kTileRows) + std::min(a.requests, a.tokens);
+}
+
+struct TileWork {
+    uint32_t request;                  // a.requests: none
+    uint32_t tiles, pieces;            // tiles of rows of the request; pieces of its longest one
+    uint32_t index;                    // among the request's (tile, piece)s, or its tiles for the join
+    uint32_t slot;                     // first workspace slot of the request (where pieces > 1)
+    uint32_t piece_tiles;              // tiles of keys in a piece
+};
+
+struct TileSearch {
+    uint64_t sum[4];
+    uint32_t key[256], count[256], slots[256], who[256], wave[4][2], found[5];
+};
+
+// Where number `index` of the (tile, piece)s of one head is, or for the join
+// number `index` of the tiles of requests that are in pieces.  At most
+// tile_bound + kSlots / heads of the former, kSlots / heads of the latter, and
+// 2 kSlots workspace slots over all heads: a request in pieces has fewer than
+// 2 tiles * keys / piece of them.
+template <int kSlots, bool kJoin>
+__device__ __forceinline__ TileWork find_work(const AttentionLaunch& a, uint32_t index, uint32_t& flags, TileSearch& s) {
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto measure = [&](uint32_t b, uint32_t& tiles, uint32_t& keys, uint32_t& f) __attribute__((always_inline)) {
+        const Span sp = span_of(a, b, f);
+        tiles = (sp.n * a.group + kTileRows - 1) / kTileRows;
+        keys = tiles ? (keys_for(a, sp, ~0u) + kTileKeys - 1) / kTileKeys : 0;
+    };
+    uint64_t all = 0;
+    uint32_t tiles = 0, keys = 0, ignore = 0;
+    for (uint32_t b = tid; b < a.requests; b += 256) {
+        measure(b, tiles, keys, flags);
+        all += uint64_t(tiles) * keys;
+    }
+    for (uint32_t d = 32; d; d >>= 1) all += __shfl_xor(all, d);
+    if (lane == 0) s.sum[wave] = all;
+    if (tid == 0) s.found[0] = a.requests;
+    __syncthreads();
+    all = (s.sum[0] + s.sum[1] + s.sum[2] + s.sum[3]) * a.heads;
+    const uint32_t piece = max(kLeastPiece, uint32_t((all + kSlots - 1) / kSlots));
+    uint32_t before = 0, slot0 = 0;
+    for (uint32_t base = 0; base < a.requests; base += 256) {
+        const uint32_t b = base + tid, n = min(256u, a.requests - base);
+        if (b >= a.requests) tiles = keys = 0;
+        else if (a.requests > 256) measure(b, tiles, keys, ignore);
+        // the longest first
+        s.key[tid] = keys;
+        __syncthreads();
+        uint32_t rank = 0;
+        for (uint32_t x = 0; x < n; ++x) rank += s.key[x] > keys || (s.key[x] == keys && x < tid);
+        if (tid < n) {
+            const uint32_t pieces = max(1u, (keys + piece - 1) / piece);
+            s.count[rank] = kJoin ? (pieces > 1 ? tiles : 0) : tiles * pieces;
+            s.slots[rank] = pieces > 1 ? tiles * pieces : 0;
+            s.who[rank] = tid;
+        }
+        __syncthreads();
+        uint32_t x = tid < n ? s.count[tid] : 0, y = tid < n ? s.slots[tid] : 0;
+        const uint32_t own = x, own_slots = y;
+        for (uint32_t d = 1; d < 64; d <<= 1) {
+            const uint32_t u = __shfl_up(x, d), v = __shfl_up(y, d);
+            if (lane >= d) {
+                x += u;
+                y += v;
+            }
+        }
+        if (lane == 63) {
+            s.wave[wave][0] = x;
+            s.wave[wave][1] = y;
+        }
+        __syncthreads();
+        uint32_t total = 0, total_slots = 0;
+        for (uint32_t w = 0; w < 4; ++w) {
+            if (w < wave) {
+                x += s.wave[w][0];
+                y += s.wave[w][1];
+            }
+            total += s.wave[w][0];
+            total_slots += s.wave[w][1];
+        }
+        const uint32_t end = before + x;
+        if (own && index >= end - own && index < end) {
+            s.found[0] = base + s.who[tid];
+            s.found[1] = index - (end - own);
+            s.found[2] = slot0 + y - own_slots;
+        }
+        before += total;
+        slot0 += total_slots;
+        if (index < before) break;
+    }
+    __syncthreads();
+    TileWork t{};
+    t.request = __builtin_amdgcn_readfirstlane(s.found[0]);
+    if (t.request >= a.requests) return t;
+    t.index = __builtin_amdgcn_readfirstlane(s.found[1]);
+    t.slot = __builtin_amdgcn_readfirstlane(s.found[2]);
+    t.piece_tiles = __builtin_amdgcn_readfirstlane(piece);
+    measure(t.request, t.tiles, keys, ignore);
+    t.pieces = max(1u, (keys + t.piece_tiles - 1) / t.piece_tiles);
+    return t;
 }
 
 template <int D>
@@ -724,17 +888,17 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
     using G = TileGeo<D, kE4m3>;
     constexpr int kWaveRows = kTileKeys / 4, kLoads = kWaveRows * T::kRow / 1024, kLanes = 64 / T::kRowsPerLoad;
     __shared__ __align__(1024) uint8_t s_tiles[2][G::kStage];
-    __shared__ uint32_t s_at;
+    __shared__ TileSearch s_search;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t head = blockIdx.x % a.heads, tile = tile_count(a) - 1 - blockIdx.x / a.heads, split = blockIdx.y;
+    const uint32_t head = blockIdx.x % a.heads;
     uint32_t flags = 0;
-    const TilePlace place = find_tile(a, tile, flags, &s_at);
-    if (blockIdx.x == 0 && split == 0 && flags && a.status) atomicOr(a.status, flags);
+    const TileWork at = find_work<tile_slots(D), false>(a, blockIdx.x / a.heads, flags, s_search);
+    if (blockIdx.x == 0 && flags && a.status) atomicOr(a.status, flags);
     flags = 0;
-    if (place.request >= a.requests) return;
-    const uint32_t b = place.request;
-    const Span sp = place.span;
-    const uint32_t rows = sp.n * a.group, row = place.row + 32 * wave + (lane & 31);
+    if (at.request >= a.requests) return;
+    const uint32_t b = at.request, tile = at.tiles - 1 - at.index / at.pieces, piece = at.index % at.pieces;
+    const Span sp = span_of(a, b, flags);
+    const uint32_t rows = sp.n * a.group, row = tile * kTileRows + 32 * wave + (lane & 31);
     const uint32_t qi = row / a.group, qg = row - qi * a.group, qh = head * a.group + qg;
     const bool have = row < rows;
     const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
@@ -745,13 +909,13 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
     const int first = int(sp.len) - int(sp.n);
     const int limit = !have ? -1 : a.causal ? first + int(qi) : int(sp.len) - 1;
     // of the wave's rows: the keys that all of them see, and the keys that any of them sees
-    const uint32_t wave_row = place.row + 32 * wave;
+    const uint32_t wave_row = tile * kTileRows + 32 * wave;
     const int all_see = wave_row >= rows ? 0 : a.causal ? max(first + int(wave_row / a.group) + 1, 0) : int(sp.len);
     const int any_sees = wave_row >= rows ? 0 : int(keys_for(a, sp, wave_row + 31));
-    const uint32_t keys = keys_for(a, sp, place.row + kTileRows - 1);
-    const uint32_t tiles = (keys + kTileKeys - 1) / kTileKeys;
-    const uint32_t begin = uint32_t(uint64_t(tiles) * split / gridDim.y) * kTileKeys;
-    const uint32_t end = min(uint32_t(uint64_t(tiles) * (split + 1) / gridDim.y) * kTileKeys, keys);
+    const uint32_t keys = keys_for(a, sp, tile * kTileRows + kTileRows - 1), span = at.piece_tiles * kTileKeys;
+    const bool whole = keys <= span;                   // these rows have one piece
+    const uint32_t begin = min(piece * uint64_t(span), uint64_t(keys)), end = min(begin + uint64_t(span), uint64_t(keys));
+    if (piece && begin == end) return;                 // earlier rows see fewer keys than the request's last
     Rows<D> st;
     st.clear();
 
@@ -762,7 +926,7 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
     // a wave brings in 16 of the 64 keys; lane j looks up the j-th of them
     auto token_of = [&](uint32_t at) { return min(at + wave * kWaveRows + (lane & 15), sp.len - 1); };
     auto look_up = [&](uint32_t at) { return a.table[int64_t(b) * a.table_stride + (token_of(at) >> a.page_shift)]; };
-    auto load_tile = [&](uint32_t at, int32_t entry, uint32_t stage) {
+    auto load_tile = [&](uint32_t at, int32_t entry, uint32_t stage) __attribute__((always_inline)) {
         const uint32_t token = token_of(at);
         bool bad = false;
         const uint32_t page = page_or_zero(entry, a.pages, &bad);
@@ -780,7 +944,7 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
         int32_t entry = look_up(begin), next = look_up(begin + kTileKeys);
         load_tile(begin, entry, 0);
         uint32_t stage = 0, t0 = begin;
-        auto advance = [&] {               // tile t0 is there; the one after it is on its way
+        auto advance = [&]() __attribute__((always_inline)) {               // tile t0 is there; the one after it is on its way
             wait_loads();
             __syncthreads();
             if (t0 + kTileKeys < end) {
@@ -798,8 +962,10 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
         for (; t0 < end; t0 += kTileKeys, stage ^= 1) advance();
     }
     const float l = half_sum(st.l);
-    if (gridDim.y > 1) {
-        float* slot = tile_slot<D>(work, (uint64_t(tile) * a.heads + head) * gridDim.y + split);
+    if (!whole) {
+        const uint64_t id = uint64_t(at.slot + at.index) * a.heads + head;
+        if (id >= a.slots) return;                     // only where requests' rows overlap
+        float* slot = tile_slot<D>(work, id);
         const uint32_t r0 = 32 * wave + (lane & 31);
         if (have) {
 #pragma unroll
@@ -837,84 +1003,74 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(256) attention_tile_combine(AttentionLaunch a, void* work, uint32_t splits) {
-    __shared__ uint32_t s_at, s_bad[4];
-    const uint32_t tid = threadIdx.x, head = blockIdx.x % a.heads, tile = blockIdx.x / a.heads;
+__global__ void __launch_bounds__(256) attention_tile_combine(AttentionLaunch a, void* work) {
+    __shared__ TileSearch s_search;
+    __shared__ uint32_t s_bad[4];
+    const uint32_t tid = threadIdx.x, head = blockIdx.x % a.heads;
     uint32_t flags = 0;
-    const TilePlace place = find_tile(a, tile, flags, &s_at);
-    if (place.request >= a.requests) return;
-    const Span sp = place.span;
-    const uint32_t rows = min(kTileRows, sp.n * a.group - place.row);
+    const TileWork at = find_work<tile_slots(D), true>(a, blockIdx.x / a.heads, flags, s_search);
+    if (at.request >= a.requests) return;
+    const Span sp = span_of(a, at.request, flags);
+    const uint32_t row0 = (at.tiles - 1 - at.index) * kTileRows;
+    const uint32_t keys = keys_for(a, sp, row0 + kTileRows - 1), span = at.piece_tiles * kTileKeys;
+    if (keys <= span) return;
+    const uint32_t pieces = (keys + span - 1) / span;
+    const uint64_t slot0 = at.slot + uint64_t(at.index) * at.pieces;
+    if ((slot0 + pieces) * a.heads > a.slots) return;
+    const uint32_t rows = min(kTileRows, sp.n * a.group - row0);
     const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
     if (tid < 4) s_bad[tid] = 0;
     __syncthreads();
     for (uint32_t i = tid; i < rows * (D / 4); i += 256) {
         const uint32_t r = i / (D / 4), f = i % (D / 4);
-        float top = -INFINITY, l = 0.0f;
-        f32x4 o{0, 0, 0, 0};
-        for (uint32_t p = 0; p < splits; ++p) {
-            const float* slot = tile_slot<D>(work, (uint64_t(tile) * a.heads + head) * splits + p);
-            const float m = slot[kTileRows * D + r], next = fmaxf(top, m);
-            const float keep = exp2_diff(top, next), add = exp2_diff(m, next);
-            l = l * keep + slot[kTileRows * (D + 1) + r] * add;
-            o = o * keep + *reinterpret_cast<const f32x4*>(slot + r * D + 4 * f) * add;
-            top = next;
-        }
-        const uint32_t row = place.row + r, qi = row / a.group, qh = head * a.group + row - qi * a.group;
+        const Joined j = join_parts<D>(0, pieces, kTileRows, r, f, [&](uint32_t p) -> const float* {
+            return tile_slot<D>(work, (slot0 + p) * a.heads + head);
+        });
+        const uint32_t row = row0 + r, qi = row / a.group, qh = head * a.group + row - qi * a.group;
         const bool none = keys_for(a, sp, row) == 0;
-        const bool nan = store_out(a, sp.row + qi, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : o * (vs / l));
+        const bool nan = store_out(a, sp.row + qi, qh, 4 * f, none ? f32x4{0, 0, 0, 0} : j.o * (vs / j.l));
         if (nan && a.causal) atomicOr(&s_bad[r >> 5], 1u << (r & 31));
-        if (f == 0) store_lse(a, sp.row + qi, qh, none ? -INFINITY : top, none ? 1.0f : l);
+        if (f == 0) store_lse(a, sp.row + qi, qh, none ? -INFINITY : j.m, none ? 1.0f : j.l);
     }
     __syncthreads();
     for (uint32_t bad = s_bad[tid >> 6]; bad; bad &= bad - 1) {
-        const uint32_t row = place.row + 32 * (tid >> 6) + __builtin_ctz(bad);
-        row_plain<D, kE4m3>(a, place.request, sp, row / a.group, head * a.group + row % a.group, flags);
+        const uint32_t row = row0 + 32 * (tid >> 6) + __builtin_ctz(bad);
+        row_plain<D, kE4m3>(a, at.request, sp, row / a.group, head * a.group + row % a.group, flags);
     }
 }
 
-// A request's rows decide which kernel computes it; the host knows only the
-// largest number of new tokens, and that a batch as full as it can be has
-// that many in every request.
-bool has_few(const AttentionLaunch& a) {
-    return a.max_new * uint64_t(a.group) <= kSplitRows || uint64_t(a.max_new) * a.requests > a.tokens;
-}
+// Where no request can have more than 32 rows the split kernel takes the
+// batch; else the tile kernel takes all of it, requests with few rows too: of
+// their tiles only the waves that have rows compute, and the keys still come
+// at the rate of the memory.
+bool few_rows(const AttentionLaunch& a) { return a.max_new * uint64_t(a.group) <= kSplitRows; }
 
-bool has_many(const AttentionLaunch& a) { return a.max_new * uint64_t(a.group) > kSplitRows; }
-
-// Runs that the keys of a tile are cut into: enough for two workgroups a CU,
-// each run at least 8 tiles of keys long where every request is as long as
-// its table allows.
-uint32_t splits_of(const AttentionLaunch& a) {
-    const uint64_t groups = uint64_t(tile_count(a)) * a.heads;
-    const uint64_t most = ((uint64_t(a.width) << a.page_shift) + 8 * kTileKeys - 1) / (8 * kTileKeys);
-    return uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({512 / groups, most, 32})));
+// Workspace slots of the tile kernel: as many as find_work gives out, or as the longest table can need.
+uint32_t slots_of(const AttentionLaunch& a, int head_dim) {
+    const uint64_t keys = ((uint64_t(a.width) << a.page_shift) + kTileKeys - 1) / kTileKeys;
+    const uint64_t most = uint64_t(tile_bound(a)) * a.heads * ((keys + kLeastPiece - 1) / kLeastPiece);
+    return uint32_t(std::min<uint64_t>(2 * tile_slots(head_dim), most));
 }
 
 template <int D, bool kE4m3>
 hipError_t launch(AttentionLaunch a, void* work, hipStream_t stream) {
-    a.least_rows = has_few(a) ? kSplitRows : 0;
-    if (has_few(a)) {
+    a.slots = slots_of(a, D);
+    if (few_rows(a)) {
         attention_split<D, kE4m3><<<kParts, Split<D, kE4m3>::kWaves * 64, 0, stream>>>(a, work);
         attention_combine<D, kE4m3><<<dim3(a.heads, a.requests), 256, 0, stream>>>(a, work);
-    }
-    if (has_many(a)) {
-        const uint32_t splits = splits_of(a), groups = tile_count(a) * a.heads;
-        attention_tiles<D, kE4m3><<<dim3(groups, splits), 256, 0, stream>>>(a, work);
-        if (splits > 1) attention_tile_combine<D, kE4m3><<<groups, 256, 0, stream>>>(a, work, splits);
+    } else {
+        const uint32_t extra = tile_slots(D) / a.heads + 1;
+        attention_tiles<D, kE4m3><<<(tile_bound(a) + extra) * a.heads, 256, 0, stream>>>(a, work);
+        attention_tile_combine<D, kE4m3><<<extra * a.heads, 256, 0, stream>>>(a, work);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
-// The two kernels' parts may share the memory: the stream runs one after the other.
 uint64_t attention_work_bytes(const AttentionLaunch& a, uint32_t head_dim) {
-    uint64_t need = 256;
-    if (has_few(a)) need = std::max<uint64_t>(need, uint64_t(kParts) * 2 * kSplitRows * (head_dim + 2) * 4);
-    if (has_many(a) && splits_of(a) > 1)
-        need = std::max<uint64_t>(need, uint64_t(tile_count(a)) * a.heads * splits_of(a) * kTileRows * (head_dim + 2) * 4);
-    return need;
+    if (few_rows(a)) return uint64_t(kParts) * 2 * kSplitRows * (head_dim + 2) * 4;
+    return std::max<uint64_t>(256, uint64_t(slots_of(a, int(head_dim))) * kTileRows * (head_dim + 2) * 4);
 }
 
 hipError_t launch_attention(const AttentionLaunch& a, uint32_t head_dim, uint32_t dtype, void* work,

@@ -14,7 +14,8 @@ constexpr uint32_t kMaxRequests = 65535;
 constexpr uint32_t kMaxGroup = 64;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-bool stride16(int64_t elements, uint32_t eb) { return (elements * int64_t(eb)) % 16 == 0; }
+// A stride keeps 16-byte alignment; that of a dimension of one element is never used.
+bool stride16(int64_t elements, uint32_t eb, uint32_t size) { return size <= 1 || (elements * int64_t(eb)) % 16 == 0; }
 
 int shift_of(uint32_t page_tokens) {
     if (page_tokens < 8 || page_tokens > 1024 || (page_tokens & (page_tokens - 1))) return -1;
@@ -30,8 +31,9 @@ int check_pages(const skv_pages* pg, const void* k, const void* v) {
         uint64_t(pg->pages) * pg->page_tokens > kMaxSlots)
         return SKV_ERR_SHAPE;
     const uint32_t eb = skv::elem_bytes(pg->dtype);
-    if (!aligned16(k) || !aligned16(v) || !stride16(pg->page_stride, eb) || !stride16(pg->token_stride, eb) ||
-        !stride16(pg->head_stride, eb) || (pg->layers > 1 && !stride16(pg->layer_stride, eb)))
+    if (!aligned16(k) || !aligned16(v) || !stride16(pg->page_stride, eb, pg->pages) ||
+        !stride16(pg->token_stride, eb, pg->page_tokens) || !stride16(pg->head_stride, eb, pg->heads) ||
+        !stride16(pg->layer_stride, eb, pg->layers))
         return SKV_ERR_ARG;
     return SKV_OK;
 }
@@ -49,8 +51,8 @@ int page_rows(const skv_pages* pg, void* k_pages, void* v_pages, const skv_rows*
     if (rows->tokens == 0) return SKV_OK;
     if (!k || !v || !slots) return SKV_ERR_ARG;
     const uint32_t eb = skv::elem_bytes(rows->dtype);
-    if (!aligned16(k) || !aligned16(v) || !stride16(rows->token_stride, eb) || !stride16(rows->head_stride, eb) ||
-        (pg->layers > 1 && !stride16(rows->layer_stride, eb)))
+    if (!aligned16(k) || !aligned16(v) || !stride16(rows->token_stride, eb, rows->tokens) ||
+        !stride16(rows->head_stride, eb, pg->heads) || !stride16(rows->layer_stride, eb, pg->layers))
         return SKV_ERR_ARG;
     skv::RowsLaunch a{};
     a.k_pages = k_pages;
@@ -146,8 +148,9 @@ int skv_page_attention(const skv_pages* pages, const skv_attention* a, void* d_w
     if (a->requests > 1 && a->table_stride < int64_t(a->width)) return SKV_ERR_ARG;
     if (!a->table || !a->lens) return SKV_ERR_ARG;
     if (a->tokens && (!a->q || !a->out)) return SKV_ERR_ARG;
-    if (!aligned16(a->q) || !aligned16(a->out) || a->q_token_stride % 8 || a->q_head_stride % 8 ||
-        a->out_token_stride % 8 || a->out_head_stride % 8)
+    if (!aligned16(a->q) || !aligned16(a->out) || !stride16(a->q_token_stride, 2, a->tokens) ||
+        !stride16(a->q_head_stride, 2, a->q_heads) || !stride16(a->out_token_stride, 2, a->tokens) ||
+        !stride16(a->out_head_stride, 2, a->q_heads))
         return SKV_ERR_ARG;
     const uint32_t eb = skv::elem_bytes(pages->dtype);
     skv::AttentionLaunch l{};

@@ -53,7 +53,7 @@ struct AttentionLaunch {
     int64_t table_stride, q_token, q_head, out_token, out_head;         // elements
     uint32_t requests, tokens, heads, group, width, pages, page_shift, max_new, causal;
     float scale;
-    uint32_t least_rows;          // requests of at most this many rows are another kernel's
+    uint32_t slots;               // the workspace's, set by launch_attention
 };
 
 hipError_t launch_plan(const PlanLaunch& a, hipStream_t stream);

@@ -751,83 +751,92 @@ _PAGES, _ROWS, _ATTENTION = struct.Struct("8I4q"), struct.Struct("2I3q"), struct
 _PAGE_TYPES = {torch.bfloat16: BF16, torch.int16: BF16, torch.float8_e4m3fn: E4M3, torch.uint8: E4M3}
 
 
-def _queue(device: torch.device, call, *args) -> int:
-    """call(*args, stream) on the device's current stream, with the device current."""
-    i = device.index
+# The current stream's handle without a Python stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _queue(i: int, call, *args) -> int:
+    """call(*args, stream) on the current stream of device i, with that device current."""
     if i == torch.cuda.current_device():
-        return call(*args, torch.cuda.current_stream().cuda_stream)
+        return call(*args, _raw_stream(i))
     with torch.cuda.device(i):
-        return call(*args, torch.cuda.current_stream().cuda_stream)
+        return call(*args, _raw_stream(i))
 
 
-def _int32(t, name: str, shape: tuple, device) -> int:
-    """Address of a contiguous int32 device tensor of the given shape (None: any size)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != len(shape) or
-            any(w is not None and n != w for n, w in zip(t.shape, shape))):
-        raise ValueError(f"{name} must be an int32 device tensor of shape {shape}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return _dev(t, name)
+def _int32(t, name: str, n, i: int) -> int:
+    """Address of a contiguous int32 tensor [n] (None: any size) on device i."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 device tensor of one dimension")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    if not t.is_cuda or t.get_device() != i:
+        raise ValueError(f"{name} must be on the same device as the other tensors")
+    return t.data_ptr()
 
 
-def _table(t, requests: int, device) -> tuple[int, int, int]:
+def _table(t, requests: int, i: int) -> tuple[int, int, int]:
     """(address, width, row stride) of a block table."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != requests:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2:
         raise ValueError(f"table must be an int32 device tensor [{requests}][blocks]")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"table must be on {device}")
-    width, stride = t.shape[1], t.stride(0)
-    if (width > 1 and t.stride(1) != 1) or (requests > 1 and stride < width):
+    rows, width = t.shape
+    if rows != requests:
+        raise ValueError(f"table must be an int32 device tensor [{requests}][blocks]")
+    if not t.is_cuda or t.get_device() != i:
+        raise ValueError("table must be on the same device as the other tensors")
+    stride, inner = t.stride()
+    if (width > 1 and inner != 1) or (requests > 1 and stride < width):
         raise ValueError("table rows must be contiguous and apart")
     return t.data_ptr(), width, stride
 
 
-def _scale_arg(t, name: str, heads: int, device) -> int:
+def _scale_arg(t, name: str, heads: int, i: int) -> int:
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or tuple(t.shape) != (heads,):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.dim() != 1 or t.numel() != heads:
         raise ValueError(f"{name} must be a float32 device tensor [{heads}]")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return _dev(t, name)
+    if not t.is_cuda or t.get_device() != i or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on the same device as the other tensors")
+    return t.data_ptr()
 
 
-def _status_arg(t, device) -> int:
-    return 0 if t is None else _int32(t, "status", (1,), device)
+def _status_arg(t, i: int) -> int:
+    return 0 if t is None else _int32(t, "status", 1, i)
 
 
-def _strides(t: torch.Tensor, name: str, written: bool) -> list:
-    """Strides, 0 for dimensions of one element; the last one must be 1."""
-    st = [0 if n == 1 else s for n, s in zip(t.shape, t.stride())]
-    if t.shape[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{name}: head_dim must be contiguous")
-    if written and any(s == 0 and n > 1 for n, s in zip(t.shape, st)):
+def _strides(shape, st: tuple, name: str, written: bool) -> tuple:
+    """Strides, of which the last must be 1 (the library passes over those of dimensions of one element)."""
+    if st[-1] != 1:
+        if shape[-1] != 1:
+            raise ValueError(f"{name}: head_dim must be contiguous")
+        st = (*st[:-1], 1)
+    if written and 0 in st and any(s == 0 and n > 1 for n, s in zip(shape, st)):
         raise ValueError(f"{name} is written to and must not be an expanded tensor")
     return st
 
 
-def _kv_pair(k, v, name: str, dims: tuple, written: bool) -> tuple[int, list]:
-    """(dtype code, strides) of two device tensors of one shape, type and strides."""
-    for t in (k, v):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() not in dims:
-            raise ValueError(f"k_{name} and v_{name} must be device tensors of {' or '.join(map(str, dims))} dimensions")
-    code = _PAGE_TYPES.get(k.dtype)
-    if code is None or v.dtype is not k.dtype or v.shape != k.shape or v.device != k.device:
+def _kv_pair(k, v, name: str, dims: tuple, written: bool) -> tuple:
+    """(dtype code, shape, strides, device) of two device tensors of one shape, type and strides."""
+    if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or not k.is_cuda or not v.is_cuda:
+        raise ValueError(f"k_{name} and v_{name} must be device tensors")
+    code, shape, i = _PAGE_TYPES.get(k.dtype), k.shape, k.get_device()
+    if len(shape) not in dims:
+        raise ValueError(f"k_{name} and v_{name} must have {' or '.join(map(str, dims))} dimensions")
+    if code is None or v.dtype is not k.dtype or v.shape != shape or v.get_device() != i:
         raise ValueError(f"k_{name} and v_{name}: one shape, device and type (bfloat16 or int16, float8_e4m3fn or uint8)")
-    st = _strides(k, "k_" + name, written)
-    if st != _strides(v, "v_" + name, written):
+    ks, vs = k.stride(), v.stride()
+    st = _strides(shape, ks, "k_" + name, written)
+    if ks != vs and any(n > 1 and a != b for n, a, b in zip(shape, ks, vs)):
         raise ValueError(f"k_{name} and v_{name} must have the same strides")
-    return code, st
+    return code, shape, st, i
 
 
-def _pool(k_pages, v_pages, written: bool, dims: tuple = (4, 5)) -> tuple[bytes, int, torch.Size, int]:
-    """(packed skv_pages, dtype code, shape, layers) of a pool of pages."""
-    code, st = _kv_pair(k_pages, v_pages, "pages", dims, written)
-    shape = k_pages.shape
-    layers = shape[0] if len(shape) == 5 else 1
-    pages, page_tokens, heads, dim = shape[-4:]
-    return (_PAGES.pack(ABI_VERSION, code, layers, pages, page_tokens, heads, dim, 0,
-                        st[0] if len(st) == 5 else 0, st[-4], st[-3], st[-2]), code, shape, layers)
+def _pool(k_pages, v_pages, written: bool, dims: tuple = (4, 5)) -> tuple:
+    """(packed skv_pages, shape, device) of a pool of pages."""
+    code, shape, st, i = _kv_pair(k_pages, v_pages, "pages", dims, written)
+    if len(shape) == 5:
+        return _PAGES.pack(ABI_VERSION, code, *shape, 0, *st[:4]), shape, i
+    return _PAGES.pack(ABI_VERSION, code, 1, *shape, 0, 0, *st[:3]), shape, i
 
 
 def page_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: torch.Tensor | None, page_tokens: int,
@@ -841,40 +850,40 @@ def page_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
     and taken [requests + 1]; taken[-1] pages of the list are then in use."""
     if not isinstance(lens, torch.Tensor) or lens.dim() != 1 or not lens.is_cuda:
         raise ValueError("lens must be an int32 device tensor [requests]")
-    device, n = lens.device, lens.shape[0]
-    pl, pn = _int32(lens, "lens", (None,), device), _int32(new, "new", (n,), device)
-    pt, width, stride = _table(table, n, device)
-    pf, nf = (0, 0) if free is None else (_int32(free, "free", (None,), device), free.shape[0])
+    i, n = lens.get_device(), lens.numel()
+    pl, pn = _int32(lens, "lens", None, i), _int32(new, "new", n, i)
+    pt, width, stride = _table(table, n, i)
+    pf, nf = (0, 0) if free is None else (_int32(free, "free", None, i), free.numel())
     # an empty list is still a list, whose address torch gives as 0
     if free is not None and nf == 0:
         pf = pl
     if not 0 <= tokens < 1 << 31:
         raise ValueError("tokens must be 0 .. 2^31 - 1")
     if out is None:
-        rows = torch.empty((2, tokens), dtype=torch.int32, device=device)
-        sums = torch.empty((2, n + 1), dtype=torch.int32, device=device)
-        out = PagePlan(rows[0], rows[1], sums[0], sums[1])
-    args = (_int32(out.slots, "slots", (tokens,), device), _int32(out.positions, "positions", (tokens,), device),
-            _int32(out.starts, "starts", (n + 1,), device), _int32(out.taken, "taken", (n + 1,), device))
-    _check(_queue(device, lib().skv_page_plan, pl, pn, n, pt, width, stride, pf, nf, page_tokens, tokens, *args,
-                  _status_arg(status, device)), "skv_page_plan")
+        buf = torch.empty(2 * (tokens + n + 1), dtype=torch.int32, device=lens.device)
+        out = PagePlan(*buf.split((tokens, tokens, n + 1, n + 1)))
+        p = buf.data_ptr()
+        args = p, p + 4 * tokens, p + 8 * tokens, p + 4 * (2 * tokens + n + 1)
+    else:
+        args = (_int32(out.slots, "slots", tokens, i), _int32(out.positions, "positions", tokens, i),
+                _int32(out.starts, "starts", n + 1, i), _int32(out.taken, "taken", n + 1, i))
+    _check(_queue(i, lib().skv_page_plan, pl, pn, n, pt, width, stride, pf, nf, page_tokens, tokens, *args,
+                  _status_arg(status, i)), "skv_page_plan")
     return out
 
 
 def _rows_call(call, what, k, v, k_pages, v_pages, slots, k_scale, v_scale, status, to_pages: bool):
-    desc, code, shape, layers = _pool(k_pages, v_pages, to_pages)
-    rcode, st = _kv_pair(k, v, "rows", (len(shape) - 1,), not to_pages)
-    if k.shape[-2:] != shape[-2:] or (len(shape) == 5 and k.shape[0] != layers):
-        raise ValueError(f"rows {tuple(k.shape)} do not fit pages {tuple(shape)}")
-    device, tokens = k.device, k.shape[-3]
-    if k_pages.device != device:
+    desc, shape, i = _pool(k_pages, v_pages, to_pages)
+    rcode, rshape, st, ri = _kv_pair(k, v, "rows", (len(shape) - 1,), not to_pages)
+    if rshape[-2:] != shape[-2:] or (len(shape) == 5 and rshape[0] != shape[0]):
+        raise ValueError(f"rows {tuple(rshape)} do not fit pages {tuple(shape)}")
+    if ri != i:
         raise ValueError("rows and pages must be on one device")
+    tokens, heads = rshape[-3], shape[-2]
     rows = _ROWS.pack(rcode, tokens, st[0] if len(shape) == 5 else 0, st[-3], st[-2])
-    ps = _int32(slots, "slots", (tokens,), device)
-    heads = shape[-2]
-    _check(_queue(device, call, desc, k_pages.data_ptr(), v_pages.data_ptr(), rows, k.data_ptr(), v.data_ptr(), ps,
-                  _scale_arg(k_scale, "k_scale", heads, device), _scale_arg(v_scale, "v_scale", heads, device),
-                  _status_arg(status, device)), what)
+    _check(_queue(i, call, desc, k_pages.data_ptr(), v_pages.data_ptr(), rows, k.data_ptr(), v.data_ptr(),
+                  _int32(slots, "slots", tokens, i), _scale_arg(k_scale, "k_scale", heads, i),
+                  _scale_arg(v_scale, "v_scale", heads, i), _status_arg(status, i)), what)
 
 
 def page_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor,
@@ -921,64 +930,69 @@ def page_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor
     bound on a request's new tokens (None: tokens).  scale: 1 / sqrt(head_dim)
     when None.  Returns out like q, or (out, lse) with lse=True or an fp32
     [tokens][q_heads] tensor to fill.  Rows of no request are left as they
-    were in `out` and lse.  work: a uint8 workspace of at least
-    page_attention_workspace(...) bytes to use in place of one from torch's
-    allocator; it must not be in use by another call at the same time."""
+    were in `out` and lse.  work: a uint8 workspace to use in place of one
+    from torch's allocator (SkvError(ERR_CAPACITY) where it is too small); it
+    must not be in use by another call at the same time."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype is not torch.bfloat16 or not q.is_cuda:
         raise ValueError("q must be a bfloat16 device tensor [tokens][q_heads][head_dim]")
-    desc, code, shape, _ = _pool(k_pages, v_pages, False, (4,))
-    device = q.device
-    tokens, q_heads, dim = q.shape
-    heads = shape[2]
-    if k_pages.device != device:
+    desc, shape, i = _pool(k_pages, v_pages, False, (4,))
+    if q.get_device() != i:
         raise ValueError("q and pages must be on one device")
-    if dim != shape[3]:
-        raise ValueError(f"q has head_dim {dim}, the pages {shape[3]}")
-    if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
+    qshape = q.shape
+    tokens, q_heads, dim = qshape
+    _, page_tokens, heads, page_dim = shape
+    if dim != page_dim:
+        raise ValueError(f"q has head_dim {dim}, the pages {page_dim}")
+    if not isinstance(lens, torch.Tensor):
         raise ValueError("lens must be an int32 device tensor [requests]")
-    n = lens.shape[0]
-    pl = _int32(lens, "lens", (None,), device)
-    ps = 0 if starts is None else _int32(starts, "starts", (n + 1,), device)
-    pt, width, stride = _table(table, n, device)
+    pl, n = _int32(lens, "lens", None, i), lens.numel()
+    ps = 0 if starts is None else _int32(starts, "starts", n + 1, i)
+    pt, width, stride = _table(table, n, i)
     if starts is None and tokens != n:
         raise ValueError("without starts there is one row per request")
     if out is None:
-        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=device)
-    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or out.device != device:
-        raise ValueError("out must be like q")
+        out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device)
+        os_ = (q_heads * dim, dim)
+    else:
+        if out.dtype is not torch.bfloat16 or out.shape != qshape or not out.is_cuda or out.get_device() != i:
+            raise ValueError("out must be like q")
+        os_ = _strides(qshape, out.stride(), "out", True)
     if lse is True:
-        lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=device)
+        lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=q.device)
     elif lse is False or lse is None:
         lse = None
-    elif (lse.dtype is not torch.float32 or lse.shape != (tokens, q_heads) or lse.device != device or
-          not lse.is_contiguous()):
+    elif (lse.dtype is not torch.float32 or lse.shape != (tokens, q_heads) or not lse.is_cuda or
+          lse.get_device() != i or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 tensor [tokens][q_heads]")
-    qs, os_ = _strides(q, "q", False), _strides(out, "out", True)
+    qs = _strides(qshape, q.stride(), "q", False)
     most = tokens if max_new is None else max_new
     if not 0 <= most < 1 << 32:
         raise ValueError("max_new must be 0 .. 2^32 - 1")
     args = _ATTENTION.pack(ABI_VERSION, n, tokens, q_heads, width, most, 1 if causal else 0,
                            dim ** -0.5 if scale is None else scale, stride, qs[0], qs[1], os_[0], os_[1],
                            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), pt, pl, ps,
-                           _scale_arg(k_scale, "k_scale", heads, device), _scale_arg(v_scale, "v_scale", heads, device),
-                           out.data_ptr(), 0 if lse is None else lse.data_ptr(), _status_arg(status, device))
-    need = ctypes.c_size_t()
-    _check(lib().skv_page_attention(desc, args, None, ctypes.byref(need), None), "skv_page_attention(size query)")
+                           _scale_arg(k_scale, "k_scale", heads, i), _scale_arg(v_scale, "v_scale", heads, i),
+                           out.data_ptr(), 0 if lse is None else lse.data_ptr(), _status_arg(status, i))
     if work is None:
-        work = torch.empty(need.value, dtype=torch.uint8, device=device)
-    elif work.dtype is not torch.uint8 or work.device != device:
-        raise ValueError(f"work must be a uint8 tensor on {device}")
-    size = ctypes.c_size_t(work.numel())
-    _check(_queue(device, lib().skv_page_attention, desc, args, _dev(work, "work"), ctypes.byref(size)),
-           "skv_page_attention")
+        need = ctypes.c_size_t()
+        _check(lib().skv_page_attention(desc, args, None, need, None), "skv_page_attention(size query)")
+        work = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+        size = need
+    else:
+        if work.dtype is not torch.uint8 or not work.is_cuda or work.get_device() != i or not work.is_contiguous():
+            raise ValueError("work must be a contiguous uint8 tensor on the same device as the other tensors")
+        size = ctypes.c_size_t(work.numel())
+    _check(_queue(i, lib().skv_page_attention, desc, args, work.data_ptr(), size), "skv_page_attention")
     return out if lse is None else (out, lse)
 
 
 def page_check(status: torch.Tensor) -> None:
     """Wait for the current stream and raise SkvError(ERR_PAGES), with the
     PAGES_* flags as its `flags`, if a call recorded one in the int32 [1] status."""
-    flags = ctypes.c_uint32()
-    rc = _queue(status.device, lib().skv_page_check, _status_arg(status, status.device), ctypes.byref(flags))
+    if not isinstance(status, torch.Tensor):
+        raise ValueError("status must be an int32 device tensor [1]")
+    flags, i = ctypes.c_uint32(), status.get_device()
+    rc = _queue(i, lib().skv_page_check, _status_arg(status, i), ctypes.byref(flags))
     if rc != OK:
         e = SkvError(rc, f"skv_page_check (flags {flags.value})")
         e.flags = flags.value

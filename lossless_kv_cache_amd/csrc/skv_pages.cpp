@@ -184,7 +184,8 @@ int skv_page_attention(const skv_pages* pages, const skv_attention* a, void* d_w
     if (l.max_new > a->tokens) l.max_new = a->tokens;
     l.causal = a->causal;
     l.scale = a->scale;
-    const uint64_t need = skv::attention_work_bytes(l, pages->head_dim);
+    const bool few = skv::attention_few_rows(l);
+    const uint64_t need = few ? skv::split_work_bytes(pages->head_dim) : skv::tiles_work_bytes(l, pages->head_dim);
     if (!d_work) {
         *work_bytes = need;
         return SKV_OK;
@@ -195,8 +196,9 @@ int skv_page_attention(const skv_pages* pages, const skv_attention* a, void* d_w
     }
     if (!aligned16(d_work)) return SKV_ERR_ARG;
     if (a->tokens == 0) return SKV_OK;
-    return skv::launch_attention(l, pages->head_dim, pages->dtype, d_work, stream) == hipSuccess ? SKV_OK
-                                                                                                : SKV_ERR_DEVICE;
+    const hipError_t e = few ? skv::launch_split(l, pages->head_dim, pages->dtype, d_work, stream)
+                             : skv::launch_tiles(l, pages->head_dim, pages->dtype, d_work, stream);
+    return e == hipSuccess ? SKV_OK : SKV_ERR_DEVICE;
 }
 
 int skv_page_check(const uint32_t* d_status, uint32_t* flags, hipStream_t stream) {

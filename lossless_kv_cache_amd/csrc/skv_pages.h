@@ -53,13 +53,16 @@ struct AttentionLaunch {
     int64_t table_stride, q_token, q_head, out_token, out_head;         // elements
     uint32_t requests, tokens, heads, group, width, pages, page_shift, max_new, causal;
     float scale;
-    uint32_t slots;               // the workspace's, set by launch_attention
+    uint32_t slots;               // the workspace's, set by launch_tiles
 };
 
 hipError_t launch_plan(const PlanLaunch& a, hipStream_t stream);
 hipError_t launch_rows(const RowsLaunch& a, hipStream_t stream);
-uint64_t attention_work_bytes(const AttentionLaunch& a, uint32_t head_dim);
-hipError_t launch_attention(const AttentionLaunch& a, uint32_t head_dim, uint32_t dtype, void* work,
-                            hipStream_t stream);
+// Whether every request has at most 32 query rows (the split kernel's batches).
+bool attention_few_rows(const AttentionLaunch& a);
+uint64_t split_work_bytes(uint32_t head_dim);
+uint64_t tiles_work_bytes(const AttentionLaunch& a, uint32_t head_dim);
+hipError_t launch_split(const AttentionLaunch& a, uint32_t head_dim, uint32_t dtype, void* work, hipStream_t stream);
+hipError_t launch_tiles(const AttentionLaunch& a, uint32_t head_dim, uint32_t dtype, void* work, hipStream_t stream);
 
 }  // namespace skv

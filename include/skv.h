@@ -422,6 +422,7 @@ int skv_store_stats(skv_store* store, skv_store_info* stats);
  *
  * Every call only queues kernels on the stream: it allocates nothing, never
  * waits, keeps no state between calls, and can be captured into a graph.
+ * Its arrays must not change until it is done.
  * Lengths, tables and slots are device data that the host never sees, so the
  * kernels check them: what is out of range is never followed; the request,
  * page or row concerned counts as empty, absent or skipped, as each call
@@ -517,7 +518,7 @@ int skv_page_read(const skv_pages* pages, const void* d_k_pages, const void* d_v
  *     [tokens][q_heads] contiguous or NULL.  Rows that no request has are left as
  *     they were.  out must not overlap q or the pages.
  *   q_heads a multiple of heads, q_heads / heads at most 64; requests 1..65535,
- *     tokens * q_heads and width * page_tokens at most 2^31 - 1.
+ *     tokens * q_heads at most 2^31 - 1, width * page_tokens at most 2^30.
  *   max_new: the caller's upper bound on any request's n (it chooses kernels
  *     and the launch; a request past it is not computed: SKV_PAGES_ROWS).
  * A request with lens < 0 or > width * P, or whose starts do not ascend

@@ -29,13 +29,6 @@ DEVICE = ["-x", "hip", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "
           "-munsafe-fp-atomics"]
 
 
-# Matrix instructions of the split kernel keep their results in ordinary
-# registers where the choice is free, so vector instructions reach the scores
-# without copies (bf16 caches with head_dim 256: 403 -> 370 us for 2.1 GB; the
-# tile kernel's e4m3 variant of that size is slower so: 577 -> 740 us).
-EXTRA = {"skv_attention_split.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
-
-
 def device_asm(out: str) -> str:
     """Write the gfx950 assembly of the kernels, compiled as the library
     compiles them, to `out` (for static checks of the generated code)."""
@@ -56,7 +49,7 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(out_dir, src + ".o")
         cmd = [hipcc, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
         if device:
-            cmd[1:1] = DEVICE + EXTRA.get(src, [])
+            cmd[1:1] = DEVICE
         else:
             cmd[1:1] = ["-ffp-contract=off", "-D__HIP_PLATFORM_AMD__"]
         if verbose:

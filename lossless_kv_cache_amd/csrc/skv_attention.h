@@ -122,6 +122,11 @@ struct Tile {
     }
 };
 
+// Quotients of 64-bit numbers that mostly fit 32 bits, where a division is a third as long.
+__device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t y) {
+    return (x | y) >> 32 ? x / y : uint32_t(x) / uint32_t(y);
+}
+
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return uint32_t(reinterpret_cast<uintptr_t>((SKV_LDS(const void))p));
 }
@@ -288,7 +293,7 @@ struct Joined {
 
 template <int D, class Slot>
 __device__ __forceinline__ Joined join_parts(uint32_t from, uint32_t to, uint32_t rows, uint32_t r, uint32_t f, Slot slot_of) {
-    constexpr uint32_t kAtOnce = 8;
+    constexpr uint32_t kAtOnce = 16;
     Joined j{-INFINITY, 0.0f, f32x4{0, 0, 0, 0}};
     for (uint32_t p = from; p < to; p += kAtOnce) {
         float m[kAtOnce], l[kAtOnce];

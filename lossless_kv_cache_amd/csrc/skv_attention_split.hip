@@ -190,10 +190,15 @@ __device__ Units find_units(const AttentionLaunch& a, uint32_t unit, uint32_t& f
     return u;
 }
 
-// Workgroups with work: every one of them has at least one unit.
-__device__ __forceinline__ uint64_t parts_of(uint64_t total) { return min(total, uint64_t(kParts)); }
+// Part p of P = min(total, kParts) begins at floor(total * p / P), so every one of them has at least one unit; no
+// division in either case.
+static_assert((kParts & (kParts - 1)) == 0, "a power of two");
 __device__ __forceinline__ uint64_t part_begin(uint64_t total, uint32_t part) {
-    return part < parts_of(total) ? total * part / parts_of(total) : total;
+    return total < kParts ? min(uint64_t(part), total) : total * min(part, kParts) / kParts;
+}
+// The part that has unit u: the last p with floor(total * p / P) <= u.
+__device__ __forceinline__ uint32_t part_of(uint64_t total, uint64_t u) {
+    return total < kParts ? uint32_t(u) : uint32_t(quotient((u + 1) * kParts - 1, total));
 }
 
 // Workspace: part p's slot: 32 rows of D sums, then 32 maxima (base-2 units)
@@ -266,8 +271,8 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
             units = units_of(a, b, G::kUnit, ignore);
             sp = span_of(a, b, ignore);
         }
-        head = uint32_t((u - first) / units);
-        const uint32_t c0 = uint32_t((u - first) % units), c1 = uint32_t(min(uint64_t(units), c0 + (end - u)));
+        head = uint32_t(quotient(u - first, units));
+        const uint32_t c0 = uint32_t(u - first - uint64_t(head) * units), c1 = uint32_t(min(uint64_t(units), c0 + (end - u)));
         run = c1 - c0;
         whole = run == units;
         const uint32_t qi = row / a.group, qg = row - qi * a.group;
@@ -412,14 +417,15 @@ __global__ void __launch_bounds__(256) attention_combine(AttentionLaunch a, cons
     }
     all *= a.heads;
     const uint64_t u0 = before * a.heads + uint64_t(head) * units, u1 = u0 + units;
-    // the part that has unit u: the last p with all * p / parts <= u
-    const uint32_t p0 = uint32_t(((u0 + 1) * parts_of(all) - 1) / all), p1 = uint32_t((u1 * parts_of(all) - 1) / all);
+    const uint32_t p0 = part_of(all, u0), p1 = part_of(all, u1 - 1);
     if (p0 == p1) return;              // finished by one workgroup
     const Span sp = span_of(a, b, flags);
     const uint32_t rows = sp.n * a.group, late = part_begin(all, p0) < u0;       // p0's slot: its first or its last
     const int first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;
     const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
-    for (uint32_t i = tid; i < rows * (D / 4); i += 256) {
+    // blockIdx.z: 256 of the rows' quads of values
+    const uint32_t i = blockIdx.z * 256 + tid;
+    if (i < rows * (D / 4)) {
         const uint32_t r = i / (D / 4), f = i % (D / 4);
         const Joined j = join_parts<D>(p0, p1 + 1, kSplitRows, r, f, [&](uint32_t p) -> const float* {
             return part_slot<D>(const_cast<void*>(work), p, p == p0 ? late : 0);
@@ -440,7 +446,8 @@ __global__ void __launch_bounds__(256) attention_combine(AttentionLaunch a, cons
 template <int D, bool kE4m3>
 hipError_t launch(const AttentionLaunch& a, void* work, hipStream_t stream) {
     attention_split<D, kE4m3><<<kParts, Split<D, kE4m3>::kWaves * 64, 0, stream>>>(a, work);
-    attention_combine<D, kE4m3><<<dim3(a.heads, a.requests), 256, 0, stream>>>(a, work);
+    const uint32_t quads = a.max_new * a.group * (D / 4);
+    attention_combine<D, kE4m3><<<dim3(a.heads, a.requests, std::max(1u, (quads + 255) / 256)), 256, 0, stream>>>(a, work);
     return hipGetLastError();
 }
 

@@ -206,6 +206,7 @@ struct TileWork {
     uint32_t index;                    // among the request's (tile, piece)s, or its tiles for the join
     uint32_t slot;                     // first workspace slot of the request (where pieces > 1)
     uint32_t piece_tiles;              // tiles of keys in a piece
+    uint32_t total;                    // all there are to find, where that is known (else the most there can be)
 };
 
 struct TileSearch {
@@ -246,7 +247,7 @@ __device__ __forceinline__ TileWork find_work(const AttentionLaunch& a, uint32_t
     all = (s.sum[0] + s.sum[1] + s.sum[2] + s.sum[3]) * a.heads;
     count = (s.sum[4] + s.sum[5] + s.sum[6] + s.sum[7]) * a.heads;
     const uint64_t share = count < kSlots / 2 ? kSlots - count : kSlots / 2;
-    const uint32_t piece = max(kLeastPiece, uint32_t((all + share - 1) / share));
+    const uint32_t piece = max(kLeastPiece, uint32_t(quotient(all + share - 1, share)));
     uint32_t before = 0, slot0 = 0;
     for (uint32_t base = 0; base < a.requests; base += 256) {
         const uint32_t b = base + tid, n = min(256u, a.requests - base);
@@ -299,6 +300,7 @@ __device__ __forceinline__ TileWork find_work(const AttentionLaunch& a, uint32_t
     }
     __syncthreads();
     TileWork t{};
+    t.total = a.requests <= 256 ? __builtin_amdgcn_readfirstlane(before) : ~0u;
     t.request = __builtin_amdgcn_readfirstlane(s.found[0]);
     if (t.request >= a.requests) return t;
     t.index = __builtin_amdgcn_readfirstlane(s.found[1]);
@@ -503,31 +505,37 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
     if (flags && a.status) atomicOr(a.status, flags);
 }
 
-// An item is 16 rows of a (tile of rows, head) that is in pieces; a fixed
-// number of workgroups goes through them, since there are mostly few or none
-// (512 of them look it up in 3 us, one for every possible item in 11).
+// An item is kJoinRows rows of a (tile of rows, head) that is in pieces, four
+// values a thread; a fixed number of workgroups goes through them, since
+// there are mostly few or none (1024 of them look it up in 4 us, one for
+// every possible item in 11).
+template <int D>
+constexpr uint32_t kJoinRows = 1024 / D;
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(256) attention_tile_combine(AttentionLaunch a, void* work, uint32_t per_tile) {
     __shared__ TileSearch s_search;
     __shared__ uint32_t s_bad;
     const uint32_t tid = threadIdx.x;
     uint32_t flags = 0;
-    for (uint32_t item = blockIdx.x;; item += gridDim.x) {
-        const uint32_t from = 16 * (item % per_tile), head = item / per_tile % a.heads;
+    uint32_t total = ~0u;              // of tiles in pieces
+    for (uint32_t item = blockIdx.x; item / per_tile / a.heads < total; item += gridDim.x) {
+        const uint32_t from = kJoinRows<D> * (item % per_tile), head = item / per_tile % a.heads;
         __syncthreads();
         if (tid == 0) s_bad = 0;
         const TileWork at = find_work<tile_slots(D), true>(a, item / per_tile / a.heads, flags, s_search);
         if (at.request >= a.requests) return;
+        total = at.total;
         const Span sp = span_of(a, at.request, flags);
         const uint32_t row0 = (at.tiles - 1 - at.index) * kTileRows;
         const uint32_t rows = min(kTileRows, sp.n * a.group - row0);
         const uint32_t keys = keys_for(a, sp, row0 + kTileRows - 1), span = at.piece_tiles * kTileKeys;
-        const uint32_t pieces = (keys + span - 1) / span, count = from < rows ? min(16u, rows - from) : 0;
+        const uint32_t pieces = (keys + span - 1) / span, count = from < rows ? min(kJoinRows<D>, rows - from) : 0;
         const uint64_t slot0 = at.slot + uint64_t(at.index) * at.pieces;
         if (count == 0 || keys <= span || (slot0 + pieces) * a.heads > a.slots) continue;
         const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
-        for (uint32_t i = tid; i < count * (D / 4); i += 256) {
-            const uint32_t r = from + i / (D / 4), f = i % (D / 4);
+        if (tid < count * (D / 4)) {
+            const uint32_t r = from + tid / (D / 4), f = tid % (D / 4);
             const Joined j = join_parts<D>(0, pieces, kTileRows, r, f, [&](uint32_t p) -> const float* {
                 return tile_slot<D>(work, (slot0 + p) * a.heads + head);
             });
@@ -557,9 +565,10 @@ template <int D, bool kE4m3>
 hipError_t launch(AttentionLaunch a, void* work, hipStream_t stream) {
     a.slots = slots_of(a, D);
     const uint32_t extra = tile_slots(D) / a.heads + 1;
-    const uint32_t per_tile = uint32_t(std::min<uint64_t>(kTileRows, uint64_t(a.max_new) * a.group) + 15) / 16;
+    const uint32_t per_tile = uint32_t(std::min<uint64_t>(kTileRows, uint64_t(a.max_new) * a.group) + kJoinRows<D> - 1) /
+                              kJoinRows<D>;
     attention_tiles<D, kE4m3><<<(tile_bound(a) + extra) * a.heads, 256, 0, stream>>>(a, work);
-    attention_tile_combine<D, kE4m3><<<std::min(512u, extra * a.heads * per_tile), 256, 0, stream>>>(a, work, per_tile);
+    attention_tile_combine<D, kE4m3><<<std::min(1024u, extra * a.heads * per_tile), 256, 0, stream>>>(a, work, per_tile);
     return hipGetLastError();
 }
 

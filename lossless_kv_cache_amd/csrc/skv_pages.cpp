@@ -9,6 +9,7 @@
 namespace {
 
 constexpr uint64_t kMaxSlots = 0x7fffffffull;
+constexpr uint64_t kMaxLength = 1ull << 30;      // of a request in attention: key indexes keep room above it
 constexpr uint32_t kMaxPlanRequests = 4096;
 constexpr uint32_t kMaxRequests = 65535;
 constexpr uint32_t kMaxGroup = 64;
@@ -140,7 +141,7 @@ int skv_page_attention(const skv_pages* pages, const skv_attention* a, void* d_w
         return SKV_ERR_SHAPE;
     if (a->requests == 0 || a->requests > kMaxRequests || a->width == 0 || a->q_heads == 0 ||
         a->q_heads % pages->heads != 0 || a->q_heads / pages->heads > kMaxGroup ||
-        uint64_t(a->tokens) * a->q_heads > kMaxSlots || uint64_t(a->width) * pages->page_tokens > kMaxSlots)
+        uint64_t(a->tokens) * a->q_heads > kMaxSlots || uint64_t(a->width) * pages->page_tokens > kMaxLength)
         return SKV_ERR_SHAPE;
     if (a->causal > 1 || !(a->scale == a->scale)) return SKV_ERR_ARG;
     if (!a->starts && a->tokens != a->requests) return SKV_ERR_ARG;

@@ -12,7 +12,6 @@ namespace skv {
 namespace {
 
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kWaves = kThreads / 64;
 
 // ------------------------------------------------------------------ plan
 // Exclusive sums of new tokens and pages over up to 4096 requests, then one
@@ -22,6 +21,8 @@ constexpr uint32_t kWaves = kThreads / 64;
 // workgroup's rows that fall into freshly taken blocks find their page in the
 // free list itself, not in the table entry another workgroup writes.
 
+constexpr uint32_t kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+
 // The sum saturates at 2^31 - 1; sums of valid requests never get there
 // without passing `tokens`, which is flagged.
 __device__ __forceinline__ uint32_t cap31(uint64_t x) { return x > 0x7fffffffull ? 0x7fffffffu : uint32_t(x); }
@@ -30,16 +31,16 @@ __device__ __forceinline__ PlanRequest request_at(const PlanLaunch& a, uint32_t 
     return plan_request(a.lens[b], a.fresh[b], a.width, a.page_shift);
 }
 
-__global__ void __launch_bounds__(kThreads) page_plan(PlanLaunch a) {
+__global__ void __launch_bounds__(kPlanThreads) page_plan(PlanLaunch a) {
     extern __shared__ uint32_t lds[];
     uint32_t* s_row = lds;                        // [requests + 1] first packed row of each request
     uint32_t* s_page = lds + a.requests + 1;      // [requests + 1] first taken page
-    __shared__ uint64_t s_sum[2][kWaves];
+    __shared__ uint64_t s_sum[2][kPlanWaves];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t P = 1u << a.page_shift;
     uint32_t flags = 0;
     uint64_t row0 = 0, page0 = 0;
-    for (uint32_t base = 0; base < a.requests; base += kThreads) {
+    for (uint32_t base = 0; base < a.requests; base += kPlanThreads) {
         const uint32_t b = base + tid;
         uint32_t rows = 0, pages = 0;
         if (b < a.requests) {
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) page_plan(PlanLaunch a) {
         }
         __syncthreads();
         uint64_t xa = row0, ya = page0;
-        for (uint32_t w = 0; w < kWaves; ++w) {
+        for (uint32_t w = 0; w < kPlanWaves; ++w) {
             if (w < wave) {
                 xa += s_sum[0][w];
                 ya += s_sum[1][w];
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) page_plan(PlanLaunch a) {
     }
     __syncthreads();
 
-    const uint32_t g = blockIdx.x * kThreads + tid, stride = gridDim.x * kThreads;
+    const uint32_t g = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
     for (uint32_t b = g; b <= a.requests; b += stride) {
         a.starts[b] = int32_t(min(s_row[b], a.tokens));
         a.taken[b] = int32_t(s_page[b]);
@@ -235,8 +236,8 @@ uint32_t magic(uint32_t d) { return uint32_t(((1ull << 32) + d - 1) / d); }
 
 hipError_t launch_plan(const PlanLaunch& a, hipStream_t stream) {
     const uint64_t work = std::max<uint64_t>({a.tokens, a.requests, a.free_pages ? a.requests : 0});
-    const uint32_t blocks = uint32_t(std::min<uint64_t>(std::max<uint64_t>((work + 1023) / 1024, 1), 512));
-    page_plan<<<blocks, kThreads, 8 * (a.requests + 1), stream>>>(a);
+    const uint32_t blocks = uint32_t(std::min<uint64_t>(std::max<uint64_t>((work + kPlanThreads - 1) / kPlanThreads, 1), 512));
+    page_plan<<<blocks, kPlanThreads, 8 * (a.requests + 1), stream>>>(a);
     return hipGetLastError();
 }
 

@@ -861,7 +861,7 @@ def page_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
         raise ValueError("tokens must be 0 .. 2^31 - 1")
     if out is None:
         buf = torch.empty(2 * (tokens + n + 1), dtype=torch.int32, device=lens.device)
-        out = PagePlan(*buf.split((tokens, tokens, n + 1, n + 1)))
+        out = PagePlan(*torch.split_with_sizes(buf, (tokens, tokens, n + 1, n + 1)))
         p = buf.data_ptr()
         args = p, p + 4 * tokens, p + 8 * tokens, p + 4 * (2 * tokens + n + 1)
     else:

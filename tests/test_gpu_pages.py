@@ -451,6 +451,46 @@ def test_bad_tables_and_lengths(skv, pairs):
     go(lambda t: t["starts"][2].fill_(new - 1), skv.PAGES_LENGTH | skv.PAGES_ROWS, (1, 2))
 
 
+@pytest.mark.parametrize("pages", [BF16, E4M3])
+@pytest.mark.parametrize("new", ["few", "many"])
+def test_many_requests(skv, new, pages):
+    """More requests than a workgroup has threads: empty ones, single tokens, some longer, one of them long."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    r = torch.Generator().manual_seed(22)
+    pairs = []
+    for b in range(700):
+        n = int(torch.randint(0, 70, (1,), generator=r))
+        pairs.append((n, min(n, b % 4) if new == "few" or b % 50 else n))
+    pairs[333] = (2500, 7 if new == "few" else 170)
+    s = batch(pairs, 2, 4, 64, 16, pages, g, extra_rows=5)
+    rows, status = s["starts"][-1].item(), dev([0])
+    out = filled(s["q"].shape, BF16)
+    bits(out).fill_(0x1234)
+    got = attend(skv, s, out=out, status=status)
+    compare(got, reference(s, 0.125, True), rows)
+    assert (bits(out)[rows:] == 0x1234).all() and status.item() == 0
+
+
+def test_no_new_tokens(skv):
+    """A batch none of whose requests has a query, said and unsaid: nothing is written."""
+    g = torch.Generator(device="cuda").manual_seed(16)
+    s = batch([(40, 0), (0, 0), (300, 0)], 2, 4, 128, 16, BF16, g, extra_rows=70)
+    for most in (0, 1, 8, 9, 70, None):
+        out, lse, st = filled(s["q"].shape, BF16), filled(s["q"].shape[:2], torch.float32), dev([0])
+        bits(out).fill_(0x1234)
+        before = lse.clone()
+        skv.page_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], s["starts"], most, out=out, lse=lse, status=st)
+        assert (bits(out) == 0x1234).all() and torch.equal(bits(lse), bits(before)) and st.item() == 0
+    # tokens of a request past the bound are not computed, and said so
+    t = batch([(40, 3), (50, 2)], 2, 4, 128, 16, BF16, g)
+    for most, heads in ((2, 4), (0, 4)):
+        out, st = filled(t["q"].shape, BF16), dev([0])
+        bits(out).fill_(0x1234)
+        skv.page_attention(t["q"], t["k"], t["v"], t["table"], t["lens"], t["starts"], most, out=out, status=st)
+        assert st.item() == skv.PAGES_ROWS and (bits(out)[:3] == 0x1234).all()
+        assert bool((bits(out)[3:] == 0x1234).all()) == (most == 0)
+
+
 def test_pool_past_four_gigabytes(skv):
     """Pages whose byte offsets pass 2^32 and element offsets 2^31."""
     g = torch.Generator(device="cuda").manual_seed(11)
@@ -590,6 +630,38 @@ def test_a_step_captured_and_replayed(skv):
         compare((out, lse), reference(s, dim ** -0.5, True), sum(news))
         assert (bits(out)[sum(news):] == 0x1234).all()
     cache.check()
+
+
+@pytest.mark.parametrize("pages", [BF16, E4M3])
+def test_two_graphs_of_chunks(skv, pages):
+    """Attention of chunks, some in pieces, captured into two graphs that are replayed at once on two streams, with
+    other lengths each time and eager work between: each replay is the eager result."""
+    g = torch.Generator(device="cuda").manual_seed(23)
+    sets = [batch([(3000, 60), (200, 100), (64, 40)], 2, 4, 128, 16, pages, g),
+            batch([(2000, 150), (1500, 30), (31, 20)], 2, 4, 128, 32, pages, g)]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in sets], [], []
+    for s, st in zip(sets, streams):
+        attend(skv, s)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            outs.append(skv.page_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], s["starts"], 150, lse=True))
+        graphs.append(graph)
+    full = [s["lens"].clone() for s in sets]
+    for cut in (0, 7, 30, 1, 12, 0):
+        for s, n in zip(sets, full):
+            s["lens"].copy_(torch.clamp(n - cut * 3, min=1))
+            s["q"].copy_(rnd(s["q"].shape, g))
+        torch.cuda.synchronize()
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for s, out in zip(sets, outs):
+            want = skv.page_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], s["starts"], 150, lse=True)
+            assert torch.equal(bits(out[0]), bits(want[0])) and torch.equal(bits(out[1]), bits(want[1]))
+            pairs = list(zip(s["lens"].tolist(), [n for _, n in s["pairs"]]))
+            compare(out, reference(dict(s, pairs=pairs), 128 ** -0.5, True), s["starts"][-1].item())
 
 
 @pytest.mark.parametrize("cid,mode", [(0, "RESIDUAL"), (2, "RESIDUAL_EXP")])

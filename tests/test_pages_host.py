@@ -97,6 +97,7 @@ def test_attention_refusals(skv):
         assert go(**kw)[0] == skv.ERR_ARG, kw
     for kw in (dict(abi=2), dict(requests=0), dict(requests=65536, tokens=65536), dict(width=0), dict(q_heads=0),
                dict(q_heads=20), dict(q_heads=8 * 65), dict(tokens=1 << 27, starts=A), dict(width=1 << 27, ts=1 << 27),
+               dict(width=(1 << 26) + 1, ts=1 << 27),
                dict(pg=pool(skv, layers=2)), dict(pg=pool(skv, dim=96)), dict(pg=pool(skv, dtype=skv.INT16))):
         assert go(**kw)[0] == skv.ERR_SHAPE, kw
     # a workspace too small is refused with the size needed, one out of line as an argument

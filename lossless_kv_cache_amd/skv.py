@@ -909,7 +909,7 @@ def page_read(k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor,
         lead = (k_pages.shape[0],) if k_pages.dim() == 5 else ()
         shape = (*lead, slots.numel(), *k_pages.shape[-2:])
         dt = k_pages.dtype if dtype is None else dtype
-        out = tuple(torch.empty(shape, dtype=dt, device=k_pages.device) for _ in range(2))
+        out = torch.empty((2, *shape), dtype=dt, device=k_pages.device).unbind(0)
     elif dtype is not None and any(t.dtype is not dtype for t in out):
         raise ValueError("out is not of the dtype asked for")
     k, v = out

@@ -212,6 +212,24 @@ def test_write_and_read(skv, layout, rows, pages, heads, dim, page, tokens, laye
     assert status.item() == 0
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.0, -0.0, 3.0, -0.7, 1e-30, 2.0 ** -70, 2.0 ** 70, 1e38, 1e-44, 1.1754942e-38,
+                                   1.9999999, 0.33333334, float("inf"), float("nan")])
+def test_every_bf16_divided_by_a_scale(skv, scale):
+    """All 65536 bf16 patterns into e4m3 pages: the correctly rounded quotient, rounded once more and saturated."""
+    x = torch.arange(-32768, 32768, device="cuda").to(torch.int16).view(BF16).view(4096, 1, 16)
+    pool = filled((2, 512, 8, 1, 16), E4M3)
+    slots = torch.arange(4096, device="cuda", dtype=torch.int32)
+    s = torch.full((1,), scale, device="cuda")
+    skv.page_write(x, x, pool[0], pool[1], slots, s, s)
+    y = x.double() / s.double()          # rounded to 32 bits below: one rounding of the exact quotient's 53 bits, which
+    want = y.float()                     # lie too far from a tie of 24 for 8-bit over 24-bit numbers to be off by it
+    want = torch.where(want.isnan(), want, want.clamp(-448, 448)).to(E4M3)
+    got, ref = bits(pool[0]).view(-1), bits(want).view(-1)
+    nan = (ref & 0x7F) == 0x7F
+    assert torch.equal((got & 0x7F) == 0x7F, nan)
+    assert torch.equal(got[~nan], ref[~nan]) and torch.equal(got, bits(pool[1]).view(-1))
+
+
 def test_rows_skip_what_is_no_slot(skv):
     g = torch.Generator(device="cuda").manual_seed(5)
     pool = torch.zeros((2, 6, 16, 2, 64), dtype=BF16, device="cuda")

@@ -122,6 +122,12 @@ struct Tile {
     }
 };
 
+// A value that is the same in every lane, where the compiler can see that it is.
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return uint64_t(__builtin_amdgcn_readfirstlane(uint32_t(x >> 32))) << 32 |
+           uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(x)));
+}
+
 // Quotients of 64-bit numbers that mostly fit 32 bits, where a division is a third as long.
 __device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t y) {
     return (x | y) >> 32 ? x / y : uint32_t(x) / uint32_t(y);

@@ -145,18 +145,28 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* s_wave, uin
     return x;                          // inclusive
 }
 
-// A value that is the same in every lane, where the compiler can see that it is.
-__device__ __forceinline__ uint64_t uniform(uint64_t x) {
-    return uint64_t(__builtin_amdgcn_readfirstlane(uint32_t(x >> 32))) << 32 |
-           uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(x)));
-}
-
 // The batch's units and, with find(total) naming a unit, the request it
 // belongs to and that request's first unit.  s_out: LDS for the answer.
 template <int kThreads, class Find>
 __device__ Units find_units(const AttentionLaunch& a, uint32_t unit, uint32_t& flags, Find find, uint64_t* s_wave,
                             uint64_t* s_out) {
     Units u{0, 0, a.requests};
+    if (a.requests <= 64) {            // each wave by itself, a request in each lane
+        const uint32_t lane = threadIdx.x & 63;
+        const uint32_t n = lane < a.requests ? units_of(a, lane, unit, flags) : 0;         // below 2^24
+        uint32_t x = n;
+        for (uint32_t d = 1; d < a.requests; d <<= 1) {
+            const uint32_t y = __shfl_up(x, d);
+            if (lane >= d) x += y;
+        }
+        u.total = uint64_t(__builtin_amdgcn_readlane(x, a.requests - 1)) * a.heads;
+        const uint64_t at = find(u.total), first = uint64_t(x - n) * a.heads;
+        const uint64_t here = __ballot(n && at >= first && at < first + uint64_t(n) * a.heads);
+        if (!here) return u;
+        u.request = __builtin_ctzll(here);
+        u.first = uint64_t(__builtin_amdgcn_readlane(x - n, u.request)) * a.heads;
+        return u;
+    }
     uint64_t total, at = 0, before = 0;
     const bool once = a.requests <= kThreads;           // one sum gives the total and every request's place
     if (!once) {
@@ -399,11 +409,11 @@ __global__ void __launch_bounds__(256) attention_combine(AttentionLaunch a, cons
         all += n;
         if (i < b) before += n;
     }
-    for (uint32_t d = 32; d; d >>= 1) {
+    for (uint32_t d = 1; d < 64 && d < a.requests; d <<= 1) {
         before += __shfl_xor(before, d);
         all += __shfl_xor(all, d);
     }
-    if ((tid & 63) == 0) {
+    if ((tid & 63) == 0) {          // (of a power of two of lanes that holds them all)
         s_sum[tid >> 6][0] = before;
         s_sum[tid >> 6][1] = all;
     }

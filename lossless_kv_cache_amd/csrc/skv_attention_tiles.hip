@@ -202,6 +202,7 @@ uint32_t tile_bound(const AttentionLaunch& a) {
 
 struct TileWork {
     uint32_t request;                  // a.requests: none
+    Span span;                         // its
     uint32_t tiles, pieces;            // tiles of rows of the request; pieces of its longest one
     uint32_t index;                    // among the request's (tile, piece)s, or its tiles for the join
     uint32_t slot;                     // first workspace slot of the request (where pieces > 1)
@@ -222,15 +223,63 @@ struct TileSearch {
 template <uint32_t kSlots, bool kJoin>
 __device__ __forceinline__ TileWork find_work(const AttentionLaunch& a, uint32_t index, uint32_t& flags, TileSearch& s) {
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    auto measure = [&](uint32_t b, uint32_t& tiles, uint32_t& keys, uint32_t& f) __attribute__((always_inline)) {
-        const Span sp = span_of(a, b, f);
+    auto measure = [&](const Span& sp, uint32_t& tiles, uint32_t& keys) __attribute__((always_inline)) {
         tiles = (sp.n * a.group + kTileRows - 1) / kTileRows;
         keys = tiles ? (keys_for(a, sp, ~0u) + kTileKeys - 1) / kTileKeys : 0;
     };
+    auto piece_of = [&](uint64_t all, uint64_t count) __attribute__((always_inline)) -> uint32_t {
+        const uint64_t share = count < kSlots / 2 ? kSlots - count : kSlots / 2;
+        return max(kLeastPiece, uint32_t(quotient(all + share - 1, share)));
+    };
+    if (a.requests <= 64) {
+        // each wave by itself, a request in each lane: what lies before a request is summed over the others directly
+        Span sp{0, 0, 0};
+        uint32_t tiles = 0, keys = 0;
+        if (lane < a.requests) {
+            sp = span_of(a, lane, flags);
+            measure(sp, tiles, keys);
+        }
+        uint64_t all = uint64_t(tiles) * keys;
+        uint32_t count = tiles;
+        for (uint32_t d = 1; d < 64 && d < a.requests; d <<= 1) {
+            all += __shfl_xor(all, d);
+            count += __shfl_xor(count, d);
+        }
+        // (over a power of two of lanes that holds them all)
+        all = uniform(all);
+        count = __builtin_amdgcn_readfirstlane(count);
+        const uint32_t piece = piece_of(all * a.heads, uint64_t(count) * a.heads);
+        const uint32_t pieces = max(1u, (keys + piece - 1) / piece);
+        const uint32_t slots = pieces > 1 ? tiles * pieces : 0;
+        const uint32_t own = kJoin ? (pieces > 1 ? tiles : 0) : tiles * pieces;
+        uint32_t begin = 0, slot = 0, total = 0;
+        for (uint32_t x = 0; x < a.requests; ++x) {
+            const uint32_t k = __builtin_amdgcn_readlane(keys, x), n = __builtin_amdgcn_readlane(own, x);
+            const bool first = k > keys || (k == keys && x < lane);         // the longest first
+            begin += first ? n : 0;
+            slot += first ? __builtin_amdgcn_readlane(slots, x) : 0;
+            total += n;
+        }
+        TileWork t{};
+        t.total = total;
+        t.request = a.requests;
+        const uint64_t here = __ballot(own && index >= begin && index - begin < own);
+        if (!here) return t;
+        const int at = __builtin_ctzll(here);
+        t.request = at;
+        t.span = Span{uint32_t(__builtin_amdgcn_readlane(sp.row, at)), uint32_t(__builtin_amdgcn_readlane(sp.n, at)),
+                      uint32_t(__builtin_amdgcn_readlane(sp.len, at))};
+        t.tiles = __builtin_amdgcn_readlane(tiles, at);
+        t.pieces = __builtin_amdgcn_readlane(pieces, at);
+        t.index = index - __builtin_amdgcn_readlane(begin, at);
+        t.slot = __builtin_amdgcn_readlane(slot, at);
+        t.piece_tiles = piece;
+        return t;
+    }
     uint64_t all = 0, count = 0;
     uint32_t tiles = 0, keys = 0, ignore = 0;
     for (uint32_t b = tid; b < a.requests; b += 256) {
-        measure(b, tiles, keys, flags);
+        measure(span_of(a, b, flags), tiles, keys);
         all += uint64_t(tiles) * keys;
         count += tiles;
     }
@@ -246,13 +295,12 @@ __device__ __forceinline__ TileWork find_work(const AttentionLaunch& a, uint32_t
     __syncthreads();
     all = (s.sum[0] + s.sum[1] + s.sum[2] + s.sum[3]) * a.heads;
     count = (s.sum[4] + s.sum[5] + s.sum[6] + s.sum[7]) * a.heads;
-    const uint64_t share = count < kSlots / 2 ? kSlots - count : kSlots / 2;
-    const uint32_t piece = max(kLeastPiece, uint32_t(quotient(all + share - 1, share)));
+    const uint32_t piece = piece_of(all, count);
     uint32_t before = 0, slot0 = 0;
     for (uint32_t base = 0; base < a.requests; base += 256) {
         const uint32_t b = base + tid, n = min(256u, a.requests - base);
         if (b >= a.requests) tiles = keys = 0;
-        else if (a.requests > 256) measure(b, tiles, keys, ignore);
+        else if (a.requests > 256) measure(span_of(a, b, ignore), tiles, keys);
         // the longest first
         s.key[tid] = keys;
         __syncthreads();
@@ -306,7 +354,8 @@ __device__ __forceinline__ TileWork find_work(const AttentionLaunch& a, uint32_t
     t.index = __builtin_amdgcn_readfirstlane(s.found[1]);
     t.slot = __builtin_amdgcn_readfirstlane(s.found[2]);
     t.piece_tiles = __builtin_amdgcn_readfirstlane(piece);
-    measure(t.request, t.tiles, keys, ignore);
+    t.span = span_of(a, t.request, ignore);
+    measure(t.span, t.tiles, keys);
     t.pieces = max(1u, (keys + t.piece_tiles - 1) / t.piece_tiles);
     return t;
 }
@@ -337,7 +386,7 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
     flags = 0;
     if (at.request >= a.requests) return;
     const uint32_t b = at.request, tile = at.tiles - 1 - at.index / at.pieces, piece = at.index % at.pieces;
-    const Span sp = span_of(a, b, flags);
+    const Span sp = at.span;
     const uint32_t rows = sp.n * a.group, wave_row = tile * kTileRows + 32 * wave;
     const float vs = a.v_scale ? a.v_scale[head] : 1.0f;
     const float raw = a.scale * (a.k_scale ? a.k_scale[head] : 1.0f);
@@ -526,7 +575,7 @@ __global__ void __launch_bounds__(256) attention_tile_combine(AttentionLaunch a,
         const TileWork at = find_work<tile_slots(D), true>(a, item / per_tile / a.heads, flags, s_search);
         if (at.request >= a.requests) return;
         total = at.total;
-        const Span sp = span_of(a, at.request, flags);
+        const Span sp = at.span;
         const uint32_t row0 = (at.tiles - 1 - at.index) * kTileRows;
         const uint32_t rows = min(kTileRows, sp.n * a.group - row0);
         const uint32_t keys = keys_for(a, sp, row0 + kTileRows - 1), span = at.piece_tiles * kTileKeys;

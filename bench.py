@@ -403,6 +403,8 @@ def store_probe(skv, cfg, tabs, tgt, prd, prefix_tokens=4096, prompts=64, reques
         ok = ok and hit.matched_blocks == half // 128
     ok = ok and bool(torch.equal(out, t[:, :, :half]))
     dec = sorted(dec_ms[1:])[len(dec_ms[1:]) // 2]
+    paged = paged_probe(skv, cfg, tabs, st, q, pr, t[:, :, :half], reps)
+    ok = ok and (paged is None or paged["verified"])
     cont = st.container(st.lookup(h)).clone()
     # the trace: the same requests against coded and raw prefixes in arenas of one size
     ranks = np.arange(1, prompts + 1, dtype=np.float64)
@@ -439,9 +441,53 @@ def store_probe(skv, cfg, tabs, tgt, prd, prefix_tokens=4096, prompts=64, reques
             "put_ms": round(put, 3), "put_GBps": round(raw / (put / 1e3) / 1e9, 1),
             "shared_prefix_tokens": half, "lookup_and_decode_ms": round(dec, 3),
             "lookup_and_decode_GBps": round(t.numel() * t.element_size() / 2 / (dec / 1e3) / 1e9, 1),
-            "verified": ok,
+            "verified": ok, "paged": paged,
             "trace": {"arena_bytes": arena_bytes, "prompts": prompts, "requests": requests, "zipf": zipf,
                       "coded": res["coded"], "raw": res["raw"]}}
+
+
+def paged_probe(skv, cfg, tabs, store, ids, aux, want, reps, new=128, page=16, dim=128, group=4):
+    """A request served from the store through pages: looking up its shared
+    prefix and restoring it into a paged cache (decode, then one copy of all
+    layers), then one step of `new` more tokens (plan, and per layer the new
+    rows written and their attention over prefix and chunk)."""
+    import torch
+
+    if cfg.kv != 2 or cfg.dtype not in ("bf16", "e4m3") or cfg.channels % dim:
+        return None
+    T, heads, layers = want.shape[2], cfg.channels // dim, cfg.layers
+    blocks = -(-(T + new) // page)
+    cache = skv.PageCache(skv.E4M3 if cfg.dtype == "e4m3" else skv.BF16, layers, blocks, page, heads, dim)
+    free = torch.randperm(blocks, device="cuda").to(torch.int32)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")      # noqa: E731
+    n_old, n_all, n_new = ints(T), ints(T + new), ints(new)
+    table = torch.full((1, blocks), -1, dtype=torch.int32, device="cuda")
+    qkv = torch.randn((new, heads * (group + 2), dim), device="cuda").to(torch.bfloat16)
+    q, k, v = qkv.split([heads * group, heads, heads], 1)
+    hashes = skv.block_hashes(ids)
+    restore_ms, step_ms = [], []
+    for _ in range(reps + 1):
+        torch.cuda.synchronize()
+        a = time.perf_counter()
+        hit = store.lookup(hashes)
+        plan = cache.plan(n_old, n_old, table, free, T)
+        cache.restore(store, tabs, hit.entry, aux, plan.slots, 0, 128 * hit.matched_blocks)
+        store.release(hit.entry)
+        torch.cuda.synchronize()
+        restore_ms.append((time.perf_counter() - a) * 1e3)
+        a = time.perf_counter()
+        step = cache.plan(n_all, n_new, table, free[-(-T // page):], new)
+        for layer in range(layers):
+            cache.write(layer, k, v, step.slots)
+            out = cache.attend(layer, q, table, n_all, step.starts, new)
+        torch.cuda.synchronize()
+        step_ms.append((time.perf_counter() - a) * 1e3)
+    cache.check()
+    rows = torch.stack(skv.page_read(cache.k, cache.v, plan.slots), 1).flatten(3)
+    same = bool(torch.equal(rows.view(want.dtype), want)) and bool(torch.isfinite(out).all())
+    mid = lambda x: round(sorted(x[1:])[len(x[1:]) // 2], 3)      # noqa: E731
+    return {"page_tokens": page, "restore_ms": mid(restore_ms), "new_tokens": new, "q_heads": heads * group,
+            "step_ms": mid(step_ms), "verified": same}
 
 
 def host_cpus() -> dict:

@@ -522,7 +522,8 @@ int skv_page_read(const skv_pages* pages, const void* d_k_pages, const void* d_v
  *   max_new: the caller's upper bound on any request's n (it chooses kernels
  *     and the launch; a request past it is not computed: SKV_PAGES_ROWS).
  * A request with lens < 0 or > width * P, or whose starts do not ascend
- * within tokens, counts as having no queries (SKV_PAGES_LENGTH).  Where a
+ * within tokens, counts as having no queries (SKV_PAGES_LENGTH); where starts
+ * descend, requests whose rows then overlap have no defined results.  Where a
  * table entry that a request needs names no page of the pool, page 0 is read
  * in its place and that request's results mean nothing (SKV_PAGES_PAGE).
  * Two-phase sizing: d_work == NULL sets *work_bytes to the need (at least

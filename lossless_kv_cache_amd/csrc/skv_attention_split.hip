@@ -92,10 +92,15 @@ __device__ __forceinline__ void tile_step(uint32_t kt, uint32_t vt, const bf16x8
 // and last), whose unnormalized sums go to the workspace for
 // attention_combine.
 //
-// A wave keeps two tiles of 16 KB (two waves with 32 KB for bf16 at D = 256) in LDS of its own: one
-// being used, the other on its way straight from memory, 64 KB in flight per
-// CU.  The next (request, head)'s first tile is on its way while the waves
-// of the last one are joined.
+// A wave keeps two tiles of 16 KB (two waves with 32 KB for bf16 at D = 256)
+// in LDS of its own: one being used, the other on its way straight from
+// memory, 64 KB in flight per CU.  The next (request, head)'s first tile is on
+// its way while the waves of the last one are joined.
+//
+// Bound by memory: 1.9 GB of four requests at 100000 to 131072 tokens in 330
+// us (5.7 TB/s, fetching 1.00 times the cache), 0.74 GB of 64 requests at 100
+// to 32768 tokens in e4m3 in 165 us (4.5 TB/s; 249 without the next one's
+// early start and the unit for a join).
 constexpr uint32_t kSplitRows = 32;
 
 template <int D, bool kE4m3>
@@ -465,8 +470,9 @@ hipError_t launch(const AttentionLaunch& a, void* work, hipStream_t stream) {
 
 // Where no request can have more than 32 rows this kernel takes the batch;
 // else the tile kernel takes all of it, requests with few rows too: of their
-// tiles only the waves that have rows compute, and the keys still come at the
-// rate of the memory.
+// tiles only the waves that have rows compute, which for single tokens still
+// reads at 0.6 (e4m3) to 1.0 (long bf16 contexts) of this kernel's rate, and
+// saves a batch of chunks a second pair of launches.
 bool attention_few_rows(const AttentionLaunch& a) { return a.max_new * uint64_t(a.group) <= kSplitRows; }
 
 uint64_t split_work_bytes(uint32_t head_dim) { return uint64_t(kParts) * 2 * kSplitRows * (head_dim + 2) * 4; }

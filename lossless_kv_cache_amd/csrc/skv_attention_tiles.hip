@@ -8,16 +8,18 @@
 namespace skv {
 namespace {
 
-// A tile of 64 keys for a wave that computes the scores of the next one while it turns this one's into probabilities and adds their
-// product with V: matrix and vector instructions of one wave then overlap.
-// A tile is taken in four steps of 16 keys, each with a quarter of the next
-// scores' products.
+// A tile of 64 keys, for a wave that computes the scores of the next one
+// while it turns this one's into probabilities and adds their product with V:
+// matrix and vector instructions of one wave then overlap.  A tile is taken in
+// four steps of 16 keys, each with a quarter of the next scores' products.
 //
 // m need not be the maximum: it is a reference that the sums are relative
 // to, moved only when a score passes it by 2^8 (sums and products then stay
-// below 2^8 times the number of keys, far from the end of the range, and
-// relative roundings are the same), so o is rescaled a few times per row and
-// not with every new maximum.
+// below 2^8 times the number of keys, far from the end of the range), so o is
+// rescaled a few times per row and not with every new maximum.  The price: a
+// row's largest probability is no longer exactly 1 and is rounded to bf16 like
+// the others (results 0.0021 of their 2-norm off in place of 0.0017, of which
+// the result's own rounding is 0.0016).
 constexpr float kSlack = 8.0f;
 
 template <int D, bool kE4m3>
@@ -176,11 +178,15 @@ struct Pipe {
 // tiles), which with the tiles' remainders fill the slots; with more, only
 // tiles of over twice an even share are cut.  attention_tile_combine joins the
 // pieces' unnormalized sums; tiles of one piece are finished where they are
-// computed.  Requests with the most keys
-// come first, and of a request the last rows, which see the most.  The heads
-// come fastest: eight consecutive workgroups go to the eight XCDs, so with 8
-// KV heads (or a divisor or multiple) each XCD's L2 holds the keys of its own
-// heads.
+// computed.  Requests with the most keys come first, and of a request the
+// last rows, which see the most.  The heads come fastest: eight consecutive
+// workgroups go to the eight XCDs, so with 8 KV heads (or a divisor or
+// multiple) each XCD's L2 holds the keys of its own heads.
+//
+// Bound by the matrix units and the power they may draw: 2048 rows x 4 heads
+// at 32768 keys in 0.94 to 1.10 ms (1140 to 970 TFLOP/s; the library's bf16
+// product of 8192 reaches 1219), matrix units busy 63% of the cycles at 2.0
+// GHz; e4m3 pages 1000, head_dim 64 790, 256 910 TFLOP/s.
 constexpr uint32_t kTileRows = 128, kTileKeys = 64;
 constexpr uint32_t kLeastPiece = 4;        // tiles of keys: below, joining costs more than it spreads
 

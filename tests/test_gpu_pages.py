@@ -471,15 +471,16 @@ def test_bad_tables_and_lengths(skv, pairs):
 
 @pytest.mark.parametrize("pages", [BF16, E4M3])
 @pytest.mark.parametrize("new", ["few", "many"])
-def test_many_requests(skv, new, pages):
+@pytest.mark.parametrize("requests", [64, 65, 200, 257, 700])
+def test_many_requests(skv, requests, new, pages):
     """More requests than a workgroup has threads: empty ones, single tokens, some longer, one of them long."""
     g = torch.Generator(device="cuda").manual_seed(21)
     r = torch.Generator().manual_seed(22)
     pairs = []
-    for b in range(700):
+    for b in range(requests):
         n = int(torch.randint(0, 70, (1,), generator=r))
         pairs.append((n, min(n, b % 4) if new == "few" or b % 50 else n))
-    pairs[333] = (2500, 7 if new == "few" else 170)
+    pairs[requests // 2] = (2500, 7 if new == "few" else 170)
     s = batch(pairs, 2, 4, 64, 16, pages, g, extra_rows=5)
     rows, status = s["starts"][-1].item(), dev([0])
     out = filled(s["q"].shape, BF16)

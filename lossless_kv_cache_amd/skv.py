@@ -872,18 +872,24 @@ def page_plan(lens: torch.Tensor, new: torch.Tensor, table: torch.Tensor, free: 
     return out
 
 
-def _rows_call(call, what, k, v, k_pages, v_pages, slots, k_scale, v_scale, status, to_pages: bool):
-    desc, shape, i = _pool(k_pages, v_pages, to_pages)
-    rcode, rshape, st, ri = _kv_pair(k, v, "rows", (len(shape) - 1,), not to_pages)
+def _rows_call(call, what, pool, rows, pk: int, pv: int, k_pages, v_pages, slots, k_scale, v_scale, status) -> None:
+    """Rows (type code, tokens, strides of layer, token and head; K and V at pk and pv) into or out of a checked pool."""
+    desc, shape, i = pool
+    heads = shape[-2]
+    _check(_queue(i, call, desc, k_pages.data_ptr(), v_pages.data_ptr(), _ROWS.pack(*rows), pk, pv,
+                  _int32(slots, "slots", rows[1], i), _scale_arg(k_scale, "k_scale", heads, i),
+                  _scale_arg(v_scale, "v_scale", heads, i), _status_arg(status, i)), what)
+
+
+def _row_args(k, v, pool, written: bool) -> tuple:
+    """_rows_call's description of rows that the caller passed for a pool."""
+    _, shape, i = pool
+    code, rshape, st, ri = _kv_pair(k, v, "rows", (len(shape) - 1,), written)
     if rshape[-2:] != shape[-2:] or (len(shape) == 5 and rshape[0] != shape[0]):
         raise ValueError(f"rows {tuple(rshape)} do not fit pages {tuple(shape)}")
     if ri != i:
         raise ValueError("rows and pages must be on one device")
-    tokens, heads = rshape[-3], shape[-2]
-    rows = _ROWS.pack(rcode, tokens, st[0] if len(shape) == 5 else 0, st[-3], st[-2])
-    _check(_queue(i, call, desc, k_pages.data_ptr(), v_pages.data_ptr(), rows, k.data_ptr(), v.data_ptr(),
-                  _int32(slots, "slots", tokens, i), _scale_arg(k_scale, "k_scale", heads, i),
-                  _scale_arg(v_scale, "v_scale", heads, i), _status_arg(status, i)), what)
+    return code, rshape[-3], st[0] if len(shape) == 5 else 0, st[-3], st[-2]
 
 
 def page_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor,
@@ -894,7 +900,9 @@ def page_write(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages:
     with a leading dimension of layers.  Any strides that are multiples of 16
     bytes with head_dim contiguous.  bf16 rows may go into e4m3 pages, divided
     by the float32 [heads] scales (None: 1)."""
-    _rows_call(lib().skv_page_write, "skv_page_write", k, v, k_pages, v_pages, slots, k_scale, v_scale, status, True)
+    pool = _pool(k_pages, v_pages, True)
+    _rows_call(lib().skv_page_write, "skv_page_write", pool, _row_args(k, v, pool, False), k.data_ptr(), v.data_ptr(),
+               k_pages, v_pages, slots, k_scale, v_scale, status)
 
 
 def page_read(k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype | None = None,
@@ -903,17 +911,27 @@ def page_read(k_pages: torch.Tensor, v_pages: torch.Tensor, slots: torch.Tensor,
     """Rows out of pages (see skv_page_read): k, v [tokens][heads][head_dim]
     (or with the pages' leading dimension of layers) of `dtype` (None: the
     pages' own type; e4m3 pages may be read as bfloat16), or into out = (k, v)."""
+    pool = _pool(k_pages, v_pages, False)
     if out is None:
-        if not isinstance(k_pages, torch.Tensor) or k_pages.dim() not in (4, 5) or not isinstance(slots, torch.Tensor):
-            raise ValueError("k_pages must be a device tensor of 4 or 5 dimensions and slots one of int32")
-        lead = (k_pages.shape[0],) if k_pages.dim() == 5 else ()
-        shape = (*lead, slots.numel(), *k_pages.shape[-2:])
+        if not isinstance(slots, torch.Tensor):
+            raise ValueError("slots must be an int32 device tensor [tokens]")
         dt = k_pages.dtype if dtype is None else dtype
-        out = torch.empty((2, *shape), dtype=dt, device=k_pages.device).unbind(0)
-    elif dtype is not None and any(t.dtype is not dtype for t in out):
-        raise ValueError("out is not of the dtype asked for")
-    k, v = out
-    _rows_call(lib().skv_page_read, "skv_page_read", k, v, k_pages, v_pages, slots, k_scale, v_scale, status, False)
+        code = _PAGE_TYPES.get(dt)
+        if code is None:
+            raise ValueError("rows are bfloat16 or int16, float8_e4m3fn or uint8")
+        _, shape, _ = pool
+        tokens, heads, dim = slots.numel(), shape[-2], shape[-1]
+        lead = shape[:-4]
+        both = torch.empty((2, *lead, tokens, heads, dim), dtype=dt, device=k_pages.device)
+        k, v = both.unbind(0)
+        rows = code, tokens, tokens * heads * dim, heads * dim, dim
+    else:
+        if dtype is not None and any(t.dtype is not dtype for t in out):
+            raise ValueError("out is not of the dtype asked for")
+        k, v = out
+        rows = _row_args(k, v, pool, True)
+    _rows_call(lib().skv_page_read, "skv_page_read", pool, rows, k.data_ptr(), v.data_ptr(), k_pages, v_pages, slots,
+               k_scale, v_scale, status)
     return k, v
 
 

@@ -142,16 +142,27 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // Written as assembly because the compiler would make every later LDS read
 // wait for every such load; no register is written, so nothing can be reused
 // too early.
+//
+// kOnce: what is read once and by one workgroup goes past the caches'
+// replacement (nt), which one that several workgroups read must not.
+template <bool kOnce = false>
 __device__ __forceinline__ void load_lds16(const uint8_t* g, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
-                 "v"(g)
-                 : "memory");
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds);
+    if constexpr (kOnce)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(to), "v"(g) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(g) : "memory");
 }
 // The same from a base that is the same for the wave and a byte offset per lane.
+template <bool kOnce = false>
 __device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
-                 "v"(offset), "s"(base)
-                 : "memory");
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds);
+    if constexpr (kOnce)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(to), "v"(offset), "s"(base)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base)
+                     : "memory");
 }
 // Every load above has landed and every LDS read before has its data.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }

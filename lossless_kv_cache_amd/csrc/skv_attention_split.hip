@@ -95,12 +95,14 @@ __device__ __forceinline__ void tile_step(uint32_t kt, uint32_t vt, const bf16x8
 // A wave keeps two tiles of 16 KB (two waves with 32 KB for bf16 at D = 256)
 // in LDS of its own: one being used, the other on its way straight from
 // memory, 64 KB in flight per CU.  The next (request, head)'s first tile is on
-// its way while the waves of the last one are joined.
+// its way while the last tile of this one is used and its waves are joined.
 //
-// Bound by memory: 1.9 GB of four requests at 100000 to 131072 tokens in 330
-// us (5.7 TB/s, fetching 1.00 times the cache), 0.74 GB of 64 requests at 100
-// to 32768 tokens in e4m3 in 165 us (4.5 TB/s; 249 without the next one's
-// early start and the unit for a join).
+// Bound by memory: 1.9 GB of four requests at 100000 to 131072 tokens in 306
+// us (6.2 TB/s, fetching 1.00 times the cache), 0.74 GB of 64 requests at 100
+// to 32768 tokens in e4m3 in 148 us (5.0 TB/s; 249 without the next one's
+// early start and the unit for a join).  The loads are marked as read once:
+// unmarked, the two take 343 and 163 us, and 2.1 GB in bf16 at D = 256 takes
+// 375 for 329.
 constexpr uint32_t kSplitRows = 32;
 
 template <int D, bool kE4m3>
@@ -223,12 +225,86 @@ __device__ __forceinline__ float* part_slot(void* work, uint32_t part, uint32_t 
     return static_cast<float*>(work) + (uint64_t(part) * 2 + slot) * kSplitRows * (D + 2);
 }
 
+// How a wave brings a tile of consecutive tokens of one head (the first a
+// multiple of 8) from their pages into LDS.  Eight of them share a page, so
+// addresses are worked out per eight, on the scalar unit, and a lane adds an
+// offset that is the same for every tile.  What lies behind a request's last
+// token may be anything, NaN too: there the last token stands in, and (as for
+// strides too long for 32 bits) lanes have addresses of their own.
+//
+// A lane that looks up its own token instead leaves the wave waiting for the
+// table within the tile's loads: 256 requests of 1000 tokens in e4m3 take 146
+// us that way and 132 this way, 64 of 16384 at D = 256 411 and 375 (both before
+// the loads were marked as read once).
+template <int D, bool kE4m3>
+struct Loader {
+    using G = Split<D, kE4m3>;
+    using T = Tile<D, kE4m3>;
+    static constexpr int kGroups = G::kKeys / 8, kLoads = G::kStage / 2 / 1024, kLanes = 64 / T::kRowsPerLoad;
+    static constexpr bool kShared = T::kRowsPerLoad <= 8;        // an instruction's rows share a page
+    static_assert(G::kKeys % 16 == 0 && T::kRowsPerLoad <= 16, "an instruction brings rows of at most two eights");
+
+    const __attribute__((address_space(4))) int32_t* table;
+    uint32_t last;                       // the request's last token
+
+    __device__ __forceinline__ Loader(const AttentionLaunch& a, uint32_t b, uint32_t len)
+        : table((const __attribute__((address_space(4))) int32_t*)(a.table + int64_t(b) * a.table_stride)), last(len - 1) {}
+
+    // The table's entries of the tile from `token` on, which has a token of the request.
+    __device__ __forceinline__ void look_up(const AttentionLaunch& a, uint32_t token, int32_t (&e)[kGroups]) const {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) e[g] = table[min(token + 8 * g, last) >> a.page_shift];
+    }
+
+    // Bytes from the pool's beginning to the first token of the g-th eight.
+    __device__ __forceinline__ int64_t place(const AttentionLaunch& a, uint32_t token, int g, int32_t entry,
+                                             uint32_t& flags) const {
+        bool bad = false;
+        const uint32_t page = page_or_zero(entry, a.pages, &bad);
+        if (bad) flags |= SKV_PAGES_PAGE;
+        const uint32_t in = min(token + 8 * g, last & ~7u) & ((1u << a.page_shift) - 1);
+        return int64_t(page) * a.page_stride + int64_t(in) * a.token_stride;
+    }
+
+    __device__ __forceinline__ void load(const AttentionLaunch& a, const uint8_t* kb, const uint8_t* vb, uint32_t token,
+                                         const int32_t (&e)[kGroups], uint32_t lds, uint32_t lane, uint32_t& flags) const {
+        if (token + G::kKeys <= last + 1 && a.token_stride >= 0 && a.token_stride < (1 << 26)) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int g = i * T::kRowsPerLoad / 8, g1 = kShared ? g : g + 1;
+                const int64_t at = place(a, token, g, e[g], flags), at1 = place(a, token, g1, e[g1], flags);
+                const uint32_t r = i * T::kRowsPerLoad + lane / kLanes, c = lane % kLanes;
+                const uint32_t row = (r & 7) * uint32_t(a.token_stride), to = lds + i * 1024;
+                const uint32_t ck = row + ((c ^ T::swizzle_k(r)) << 4), cv = row + ((c ^ T::swizzle_v(r)) << 4);
+                if constexpr (kShared) {
+                    load_lds16<true>(kb + at, ck, to);
+                    load_lds16<true>(vb + at, cv, to + G::kStage / 2);
+                } else {
+                    load_lds16<true>(kb + (r & 8 ? at1 : at) + ck, to);
+                    load_lds16<true>(vb + (r & 8 ? at1 : at) + cv, to + G::kStage / 2);
+                }
+            }
+        } else {
+            asm volatile("" : "+v"(lane));           // keeps what is worked out from it here, and registers free
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int g = i * T::kRowsPerLoad / 8, g1 = kShared ? g : g + 1;
+                const int64_t at = place(a, token, g, e[g], flags), at1 = place(a, token, g1, e[g1], flags);
+                const uint32_t r = i * T::kRowsPerLoad + lane / kLanes, c = lane % kLanes, to = lds + i * 1024;
+                const uint32_t row = min(r & 7, last - min(token + (r & ~7u), last & ~7u));
+                const int64_t o = (r & 8 && !kShared ? at1 : at) + int64_t(row) * a.token_stride;
+                load_lds16<true>(kb + o + ((c ^ T::swizzle_k(r)) << 4), to);
+                load_lds16<true>(vb + o + ((c ^ T::swizzle_v(r)) << 4), to + G::kStage / 2);
+            }
+        }
+    }
+};
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_split(AttentionLaunch a, void* work) {
     using G = Split<D, kE4m3>;
-    using T = Tile<D, kE4m3>;
-    constexpr int kThreads = G::kWaves * 64, kLoads = G::kStage / 2 / 1024, kLanes = 64 / T::kRowsPerLoad;
-    constexpr int kLook = G::kKeys > 64 ? 2 : 1;         // lane j looks up token j of a tile (and j + 64)
+    using L = Loader<D, kE4m3>;
+    constexpr int kThreads = G::kWaves * 64;
     __shared__ __align__(1024) uint8_t s_tiles[G::kWaves][2][G::kStage];
     __shared__ float s_m[G::kWaves][kSplitRows], s_l[G::kWaves][kSplitRows];
     __shared__ uint64_t s_wave[G::kWaves], s_found[2];
@@ -245,95 +321,106 @@ __global__ void __launch_bounds__((Split<D, kE4m3>::kWaves * 64), 1) attention_s
     const uint32_t lds0 = lds_address(&s_tiles[wave][0][0]);
     const uint32_t lane_k = lds0 + base_k<D, kE4m3>(lane), lane_v = lds0 + G::kStage / 2 + base_v<D, kE4m3>(lane);
 
-    // the request and head of unit u, the run of its units that is ours, and what its rows need
-    uint64_t u = begin, first = un.first;
+    // a run of units of one (request, head): what is ours of it, what its rows need, the wave's tiles
+    struct Run {
+        Span sp;
+        uint32_t b, head, units, t0, stop;
+        bool whole;
+        float raw;
+        int first_limit, limit;          // the last key of query 0, of the lane's row
+        const uint8_t *kb, *vb;
+    };
+    uint64_t u = begin, first = un.first;                          // the next run's first unit; its request's
     uint32_t b = un.request, units = units_of(a, b, G::kUnit, ignore);
     Span sp = span_of(a, b, ignore);
-    uint32_t head, run, t0, stop;
-    bool whole;
-    float raw;
-    int first_limit, limit;
     bf16x8 q[D / 16];
-    int32_t next[kLook];
     uint32_t stage = 1;
-    const uint8_t *kb, *vb;
-    auto look_up = [&](uint32_t at, int32_t (&e)[kLook]) __attribute__((always_inline)) {
-        for (int i = 0; i < kLook; ++i)
-            e[i] = a.table[int64_t(b) * a.table_stride + (min(at + 64 * i + lane, sp.len - 1) >> a.page_shift)];
-    };
-    auto load_tile = [&](uint32_t at, const int32_t (&e)[kLook], uint32_t to) __attribute__((always_inline)) {
-        int64_t off[kLook];
-        for (int i = 0; i < kLook; ++i) {
-            const uint32_t token = min(at + 64 * i + lane, sp.len - 1);
-            bool bad = false;
-            const uint32_t page = page_or_zero(e[i], a.pages, &bad);
-            if (bad) flags |= SKV_PAGES_PAGE;
-            off[i] = int64_t(page) * a.page_stride + int64_t(token & ((1u << a.page_shift) - 1)) * a.token_stride;
-        }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t r = i * T::kRowsPerLoad + lane / kLanes, c = lane % kLanes;
-            const int64_t o = __shfl(off[(i * T::kRowsPerLoad) / 64], int(r & 63));
-            load_lds16(kb + o + ((c ^ T::swizzle_k(r)) << 4), lds0 + to * G::kStage + i * 1024);
-            load_lds16(vb + o + ((c ^ T::swizzle_v(r)) << 4), lds0 + to * G::kStage + G::kStage / 2 + i * 1024);
-        }
-    };
-    // Unit u's (request, head): its rows' queries and its first tile, into the stage that is not in use.
-    auto open = [&]() __attribute__((always_inline)) -> bool {
+    auto find = [&](Run& x) __attribute__((always_inline)) -> bool {
+        if (u >= end) return false;
         while (units == 0 || u - first >= uint64_t(units) * a.heads) {
             first += uint64_t(units) * a.heads;
             if (++b >= a.requests) return false;
             units = units_of(a, b, G::kUnit, ignore);
             sp = span_of(a, b, ignore);
         }
-        head = uint32_t(quotient(u - first, units));
-        const uint32_t c0 = uint32_t(u - first - uint64_t(head) * units), c1 = uint32_t(min(uint64_t(units), c0 + (end - u)));
-        run = c1 - c0;
-        whole = run == units;
-        const uint32_t qi = row / a.group, qg = row - qi * a.group;
-        const bool have = row < sp.n * a.group;
-        raw = a.scale * (a.k_scale ? a.k_scale[head] : 1.0f);
-        first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;          // of query 0
-        limit = have ? first_limit + (a.causal ? int(qi) : 0) : -1;
-        kb = a.k_pages + int64_t(head) * a.head_stride;
-        vb = a.v_pages + int64_t(head) * a.head_stride;
-        t0 = c0 * G::kUnit + wave * G::kKeys;
-        stop = min(c1 * G::kUnit, sp.len);
-        if (t0 < stop) {
-            int32_t e[kLook];
-            look_up(t0, e);
-            look_up(t0 + G::kUnit, next);
-            load_q<D, kE4m3>(a.q + int64_t(sp.row + qi) * a.q_token + int64_t(head * a.group + qg) * a.q_head, have, raw,
-                             lane, q);
-            load_tile(t0, e, stage ^ 1);
-        }
+        x.sp = sp;
+        x.b = b;
+        x.head = uint32_t(quotient(u - first, units));
+        const uint32_t c0 = uint32_t(u - first - uint64_t(x.head) * units);
+        const uint32_t c1 = uint32_t(min(uint64_t(units), c0 + (end - u)));
+        x.units = c1 - c0;
+        x.whole = x.units == units;
+        const uint32_t qi = row / a.group;
+        x.raw = a.scale * (a.k_scale ? a.k_scale[x.head] : 1.0f);
+        x.first_limit = a.causal ? int(sp.len) - int(sp.n) : int(sp.len) - 1;
+        x.limit = row < sp.n * a.group ? x.first_limit + (a.causal ? int(qi) : 0) : -1;
+        x.kb = a.k_pages + int64_t(x.head) * a.head_stride;
+        x.vb = a.v_pages + int64_t(x.head) * a.head_stride;
+        x.t0 = c0 * G::kUnit + wave * G::kKeys;
+        x.stop = min(c1 * G::kUnit, sp.len);
+        u += x.units;
         return true;
     };
+    auto look_up = [&](const Run& x, uint32_t at, int32_t (&e)[L::kGroups]) __attribute__((always_inline)) {
+        L(a, x.b, x.sp.len).look_up(a, at, e);
+    };
+    auto load_tile = [&](const Run& x, uint32_t at, const int32_t (&e)[L::kGroups], uint32_t to)
+                         __attribute__((always_inline)) {
+        L(a, x.b, x.sp.len).load(a, x.kb, x.vb, at, e, lds0 + to * G::kStage, lane, flags);
+    };
+    auto load_queries = [&](const Run& x) __attribute__((always_inline)) {
+        const uint32_t qi = row / a.group, qg = row - qi * a.group;
+        load_q<D, kE4m3>(a.q + int64_t(x.sp.row + qi) * a.q_token + int64_t(x.head * a.group + qg) * a.q_head,
+                         row < x.sp.n * a.group, x.raw, lane, q);
+    };
 
-    bool more = open();
+    Run run, ahead;
+    bool more = find(run);
+    if (more && run.t0 < run.stop) {
+        int32_t e[L::kGroups];
+        look_up(run, run.t0, e);
+        load_tile(run, run.t0, e, stage ^ 1);
+        load_queries(run);
+    }
+    bool first_run = true;
     while (more) {
-        const float factor = raw == 0.0f ? 1.0f : fabsf(raw) * kLog2e;
+        const float factor = run.raw == 0.0f ? 1.0f : fabsf(run.raw) * kLog2e;
         Rows<D> st;
         st.clear();
-        for (; t0 < stop; t0 += G::kUnit) {
+        // The wave's tiles of this run, each loaded while the one before is used; with the last one in hand, the
+        // next run's first is on its way.  A wave without tiles here only does the latter.
+        const bool some = run.t0 < run.stop;
+        uint32_t t0 = run.t0;
+        auto use_tile = [&]() __attribute__((always_inline)) {
+            tile_step<D, kE4m3, G::kKeys / 32>(lane_k + stage * G::kStage, lane_v + stage * G::kStage, q, factor,
+                                               int(t0) + G::kKeys - 1 > run.first_limit, run.limit - int(t0), lane, st);
+        };
+        int32_t e[L::kGroups];
+        for (; t0 + G::kUnit < run.stop; t0 += G::kUnit) {
+            stage ^= 1;
+            look_up(run, t0 + G::kUnit, e);
+            wait_loads();
+            load_tile(run, t0 + G::kUnit, e, stage ^ 1);
+            __builtin_amdgcn_sched_barrier(0);         // all loads on their way before the tile is used
+            use_tile();
+        }
+        more = find(ahead);
+        const bool coming = more && ahead.t0 < ahead.stop;
+        if (coming) look_up(ahead, ahead.t0, e);
+        if (some) {
             stage ^= 1;
             wait_loads();
-            if (t0 + G::kUnit < stop) {
-                int32_t e[kLook];
-                for (int i = 0; i < kLook; ++i) e[i] = next[i];
-                look_up(t0 + 2 * G::kUnit, next);
-                load_tile(t0 + G::kUnit, e, stage ^ 1);
-            }
-            tile_step<D, kE4m3, G::kKeys / 32>(lane_k + stage * G::kStage, lane_v + stage * G::kStage, q, factor,
-                                               int(t0) + G::kKeys - 1 > first_limit, limit - int(t0), lane, st);
         }
+        if (coming) load_tile(ahead, ahead.t0, e, stage ^ 1);
+        if (some) use_tile();
+        if (coming) load_queries(ahead);
         // what is joined now, before the next one's state takes its place
-        const Span was = sp;
-        const uint32_t was_b = b, was_head = head, rows = sp.n * a.group, slot_at = u != begin;
-        const bool was_whole = whole;
-        const int was_limit = first_limit;
-        u += run;
-        more = u < end && open();
+        const Span was = run.sp;
+        const uint32_t was_b = run.b, was_head = run.head, rows = was.n * a.group, slot_at = !first_run;
+        const bool was_whole = run.whole;
+        const int was_limit = run.first_limit;
+        first_run = false;
+        run = ahead;
         // the sums of each wave to LDS, into the stage it used last; then every thread takes some of a row's values
         const float vs = a.v_scale ? a.v_scale[was_head] : 1.0f;
         float* slot = part_slot<D>(work, part, slot_at);

@@ -377,7 +377,12 @@ struct TileGeo {
     static constexpr int kPerCu = tile_slots(D) / 256;               // workgroups a CU holds
 };
 
-template <int D, bool kE4m3>
+// kOnce: every request has one tile of rows, so its keys are read by one
+// workgroup and marked so: 9 new tokens over each of 64 caches of 16384 in bf16
+// take 682 us for 752 at D = 128, 388 for 425 at D = 64, 612 for 625 at D =
+// 256.  Keys that tiles share must not be: a chunk of 2048 at 32768 takes 1051
+// us with the mark and 1037 without.
+template <int D, bool kE4m3, bool kOnce>
 __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_tiles(AttentionLaunch a, void* work) {
     using T = Tile<D, kE4m3>;
     using G = TileGeo<D, kE4m3>;
@@ -455,15 +460,15 @@ __global__ void __launch_bounds__(256, (TileGeo<D, kE4m3>::kPerCu)) attention_ti
                 const uint32_t chunk = (c ^ (v ? T::swizzle_v(r) : T::swizzle_k(r))) << 4;
                 const uint32_t offset = (in & 7) * uint32_t(a.token_stride) + chunk;
                 if constexpr (T::kRowsPerLoad <= 8)
-                    load_lds16(from + w.at[(i * T::kRowsPerLoad) >> 3], offset, to + i * 1024);
+                    load_lds16<kOnce>(from + w.at[(i * T::kRowsPerLoad) >> 3], offset, to + i * 1024);
                 else
-                    load_lds16(from + (in < 8 ? w.at[0] : w.at[1]) + offset, to + i * 1024);
+                    load_lds16<kOnce>(from + (in < 8 ? w.at[0] : w.at[1]) + offset, to + i * 1024);
             }
         } else {
 #pragma unroll 1
             for (int i = 0; i < kLoads; ++i) {
                 const uint32_t r = wave * kWaveRows + i * T::kRowsPerLoad + lane / kLanes, c = lane % kLanes;
-                load_lds16(from + token_at(a, b, min(at + r, sp.len - 1), flags) +
+                load_lds16<kOnce>(from + token_at(a, b, min(at + r, sp.len - 1), flags) +
                                ((c ^ (v ? T::swizzle_v(r) : T::swizzle_k(r))) << 4),
                            to + i * 1024);
             }
@@ -620,9 +625,11 @@ template <int D, bool kE4m3>
 hipError_t launch(AttentionLaunch a, void* work, hipStream_t stream) {
     a.slots = slots_of(a, D);
     const uint32_t extra = tile_slots(D) / a.heads + 1;
-    const uint32_t per_tile = uint32_t(std::min<uint64_t>(kTileRows, uint64_t(a.max_new) * a.group) + kJoinRows<D> - 1) /
-                              kJoinRows<D>;
-    attention_tiles<D, kE4m3><<<(tile_bound(a) + extra) * a.heads, 256, 0, stream>>>(a, work);
+    const uint64_t rows = uint64_t(a.max_new) * a.group;                       // of a request, at most
+    const uint32_t per_tile = uint32_t(std::min<uint64_t>(kTileRows, rows) + kJoinRows<D> - 1) / kJoinRows<D>;
+    const uint32_t grid = (tile_bound(a) + extra) * a.heads;
+    if (rows <= kTileRows) attention_tiles<D, kE4m3, true><<<grid, 256, 0, stream>>>(a, work);
+    else attention_tiles<D, kE4m3, false><<<grid, 256, 0, stream>>>(a, work);
     attention_tile_combine<D, kE4m3><<<std::min(1024u, extra * a.heads * per_tile), 256, 0, stream>>>(a, work, per_tile);
     return hipGetLastError();
 }

@@ -302,41 +302,60 @@ __device__ __forceinline__ void store_lse(const AttentionLaunch& a, uint64_t row
     if (a.lse) a.lse[row * (uint64_t(a.heads) * a.group) + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Partial sums (m in base-2 units, l, o) read kAtOnce at a time: their loads are in flight together.
+// Partial sums (m in base-2 units, l, o), joined in order.
 struct Joined {
     float m, l;
     f32x4 o;
 };
 
+// The next at most N of them: their loads are in flight together.
+template <uint32_t N, int D, class Slot>
+__device__ __forceinline__ void join_some(Joined& j, uint32_t p, uint32_t to, uint32_t rows, uint32_t r, uint32_t f,
+                                          Slot slot_of) {
+    float m[N], l[N];
+    f32x4 o[N];
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+        const float* slot = slot_of(min(p + i, to - 1));
+        m[i] = slot[rows * D + r];
+        l[i] = slot[rows * (D + 1) + r];
+        o[i] = *reinterpret_cast<const f32x4*>(slot + r * D + 4 * f);
+    }
+    float top = j.m;
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+        if (p + i >= to) m[i] = -INFINITY;
+        top = fmaxf(top, m[i]);
+    }
+    const float keep = exp2_diff(j.m, top);
+    j.l *= keep;
+    j.o *= keep;
+    j.m = top;
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) {
+        const float k = exp2_diff(m[i], top);
+        j.l += k * l[i];
+        if (m[i] != -INFINITY) j.o += k * o[i];    // else all its keys were hidden, and o may be 0 * NaN
+    }
+}
+
+// Sixteen at a time, and fewer where few are left, since a place that stands
+// for none is loaded too: 9 new tokens over each of 64 caches of 1024 tokens,
+// in pieces of 4 tiles, take 38.2 us that way and 43.8 with sixteen throughout
+// (one cache of 65536 takes 49.0 and 47.6).
 template <int D, class Slot>
 __device__ __forceinline__ Joined join_parts(uint32_t from, uint32_t to, uint32_t rows, uint32_t r, uint32_t f, Slot slot_of) {
-    constexpr uint32_t kAtOnce = 16;
     Joined j{-INFINITY, 0.0f, f32x4{0, 0, 0, 0}};
-    for (uint32_t p = from; p < to; p += kAtOnce) {
-        float m[kAtOnce], l[kAtOnce];
-        f32x4 o[kAtOnce];
-#pragma unroll
-        for (uint32_t i = 0; i < kAtOnce; ++i) {
-            const float* slot = slot_of(min(p + i, to - 1));
-            m[i] = slot[rows * D + r];
-            l[i] = slot[rows * (D + 1) + r];
-            o[i] = *reinterpret_cast<const f32x4*>(slot + r * D + 4 * f);
-        }
-        float top = j.m;
-#pragma unroll
-        for (uint32_t i = 0; i < kAtOnce; ++i) {
-            if (p + i >= to) m[i] = -INFINITY;
-            top = fmaxf(top, m[i]);
-        }
-        const float keep = exp2_diff(j.m, top);
-        j.l *= keep;
-        j.o *= keep;
-        j.m = top;
-#pragma unroll
-        for (uint32_t i = 0; i < kAtOnce; ++i) {
-            const float k = exp2_diff(m[i], top);
-            j.l += k * l[i];
-            if (m[i] != -INFINITY) j.o += k * o[i];    // else all its keys were hidden, and o may be 0 * NaN
+    for (uint32_t p = from; p < to;) {
+        if (to - p > 8) {
+            join_some<16, D>(j, p, to, rows, r, f, slot_of);
+            p += 16;
+        } else if (to - p > 4) {
+            join_some<8, D>(j, p, to, rows, r, f, slot_of);
+            p += 8;
+        } else {
+            join_some<4, D>(j, p, to, rows, r, f, slot_of);
+            p += 4;
         }
     }
     return j;

@@ -490,6 +490,27 @@ def test_many_requests(skv, requests, new, pages):
     assert (bits(out)[rows:] == 0x1234).all() and status.item() == 0
 
 
+@pytest.mark.parametrize("pages", [BF16, E4M3])
+@pytest.mark.parametrize("dim,page", [(64, 8), (128, 8), (256, 8), (64, 64), (128, 32), (256, 128)])
+def test_short_and_empty_requests_in_a_row(skv, dim, page, pages):
+    """Workgroups that go through several requests each: ends inside a page and a tile, waves without tokens."""
+    g = torch.Generator(device="cuda").manual_seed(dim + page)
+    r = torch.Generator().manual_seed(dim * page)
+    lens = [0, 1, 7, 8, 9, 31, 33, 64, 65, 127, 129, 130, 257, 513]
+    pairs = []
+    for b in range(100):
+        n = lens[int(torch.randint(0, len(lens), (1,), generator=r))]
+        pairs.append((n, min(n, 1 + b % 3) if b % 7 else 0))
+    pairs[0], pairs[-1] = (513, 2), (1, 1)
+    s = batch(pairs, 4, 8, dim, page, pages, g, layout="head" if page == 8 else "token", extra_rows=2)
+    rows, status = s["starts"][-1].item(), dev([0])
+    out = filled(s["q"].shape, BF16)
+    bits(out).fill_(0x1234)
+    got = attend(skv, s, out=out, status=status)
+    compare(got, reference(s, dim ** -0.5, True), rows)
+    assert (bits(out)[rows:] == 0x1234).all() and status.item() == 0
+
+
 def test_no_new_tokens(skv):
     """A batch none of whose requests has a query, said and unsaid: nothing is written."""
     g = torch.Generator(device="cuda").manual_seed(16)

@@ -169,11 +169,12 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // Bound by memory.  One item a thread, as many workgroups as it takes: 1.2 GB
 // of e4m3 rows out of their pages in 194 us, 6.2 TB/s (four items a thread,
 // one after another 222 us, requested together 219); a prompt's 32768 rows of
-// 8 heads into e4m3 pages, 0.2 GB, in 34 us (46 with stores that stay in the
-// caches; an attention that reads the pages right after takes the same either
-// way).  Rows that keep their type are stored the ordinary way: past the caches
-// 32768 of them take 48 us for 59, but then the attention after them loses more
-// (8 prompts of 2048 tokens, both together, 348 for 344).
+// 8 heads into e4m3 pages, 0.2 GB, in 34 us (44 where the rows come from
+// memory; both 46 with stores that stay in the caches; an attention that reads
+// the pages right after takes the same either way).  Rows that keep their type
+// are stored the ordinary way: past the caches 32768 of them take 48 us for
+// 59, but then the attention after them loses more (8 prompts of 2048 tokens,
+// both together, 348 for 344).
 struct RowsGeo {
     uint32_t items;              // per token
     uint32_t per_head;           // items per head
